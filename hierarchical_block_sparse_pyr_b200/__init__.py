@@ -23,6 +23,17 @@ every call needs CUDA tensors.
     bsa_backward(shape, Q, K, V, O, lse, dO, idx, offset, rho, delta, dQ, dK, dV)
                                               gradients of the block-sparse attention
     forward(Q, K, V, b, topk, cap)            allocate outputs and run all three
+    rope_spec(d, rot, base, layout, scaling)  rotary positions: the frequencies of a head's pairs
+    rope_apply(spec, Q, K, Qo, Ko, pos)       rotate queries and keys (inverse=True: the gradient)
+    packed_shape(S, T, Hq, Hkv, d, dtype), packed_plan(shape, cu)
+                                              sequences of different lengths on one token axis
+    packed_forward(shape, Q, K, V, plan, O, lse)
+                                              causal attention of every packed sequence
+    packed_backward(shape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV)
+                                              its gradients
+    tree_shape(B, Hq, Hkv, N, T, d, dtype)
+    tree_forward(shape, Q, K, V, lens, parent, O, lse, workspace)
+                                              drafted token trees over a cache (one token: ragged decode)
 """
 from __future__ import annotations
 
@@ -34,15 +45,18 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libpyr.so")
 
-PYR_OK, PYR_EINVAL, PYR_EUNSUPPORTED, PYR_ECUDA, PYR_ETIMEOUT, PYR_EBADIDX = range(6)
+PYR_OK, PYR_EINVAL, PYR_EUNSUPPORTED, PYR_ECUDA, PYR_ETIMEOUT, PYR_EBADIDX, PYR_EBADSEQ = range(7)
 PYR_F32, PYR_BF16 = 0, 1
+PYR_TREE_ROOT, PYR_TREE_ABSENT = -1, -2
 
 ABI_SYMBOLS = ("pyr_num_levels", "pyr_num_nodes", "pyr_num_qblocks", "pyr_pyramid_elems", "pyr_build", "pyr_means",
                "pyr_update",
                "pyr_select", "pyr_select_ex", "pyr_select_trace_levels", "pyr_select_trace_width", "bsa_forward",
                "dense_forward", "bsa_forward_host", "pyr_host_workspace_bytes", "bsa_route_invert", "bsa_backward",
                "bsa_backward_noalloc", "pyr_selftest_wait", "pyr_strerror", "phba_state_elems",
-               "phba_state_workspace_bytes", "phba_state_build", "phba_forward")
+               "phba_state_workspace_bytes", "phba_state_build", "phba_forward", "rope_spec_init", "rope_apply",
+               "packed_plan_elems", "packed_plan", "packed_forward", "packed_backward", "tree_workspace_bytes",
+               "tree_forward")
 
 
 class PyrShape(ctypes.Structure):
@@ -56,6 +70,24 @@ class PyrShape(ctypes.Structure):
 class PyrSelectOpts(ctypes.Structure):
     _fields_ = [("budget", ctypes.c_void_p), ("fcf_tau", ctypes.c_float), ("fcf_extra", ctypes.c_int),
                 ("rcg_lambda", ctypes.c_float), ("trace", ctypes.c_void_p)]
+
+
+class PyrView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("row", ctypes.c_int64)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int), ("rot", ctypes.c_int), ("layout", ctypes.c_int), ("reserved", ctypes.c_int),
+                ("scale", ctypes.c_double), ("freq", ctypes.c_double * 64)]
+
+
+class PackedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("S", "T", "Hq", "Hkv", "d", "dtype")]
+
+
+class TreeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hkv", "N", "T", "d", "dtype")]
 
 
 class PyrError(RuntimeError):
@@ -115,6 +147,22 @@ def _load_lib():
     lib.phba_state_build.restype = ctypes.c_int
     lib.phba_forward.argtypes = [sp, vp, vp, vp, vp, vp, ctypes.c_int, vp, vp, vp, vp, vp, vp]
     lib.phba_forward.restype = ctypes.c_int
+    vw, ps, ts = ctypes.POINTER(PyrView), ctypes.POINTER(PackedShape), ctypes.POINTER(TreeShape)
+    i, dbl = ctypes.c_int, ctypes.c_double
+    lib.rope_spec_init.argtypes = [ctypes.POINTER(RopeSpec), i, i, i, dbl, i, dbl, i]
+    lib.rope_apply.argtypes = [ctypes.POINTER(RopeSpec), i, i, i, i, i, vw, vw, vp, ctypes.c_int64, i, vw, vw, i, vp,
+                               vp]
+    lib.packed_plan_elems.argtypes = [ps]
+    lib.packed_plan_elems.restype = ctypes.c_size_t
+    lib.packed_plan.argtypes = [ps, vp, vp, vp, vp]
+    lib.packed_forward.argtypes = [ps, vw, vw, vw, vp, vw, vp, vp, vp]
+    lib.packed_backward.argtypes = [ps, vw, vw, vw, vp, vw, vp, vw, vp, vw, vw, vw, vp, vp]
+    lib.tree_workspace_bytes.argtypes = [ts]
+    lib.tree_workspace_bytes.restype = ctypes.c_size_t
+    lib.tree_forward.argtypes = [ts, vw, vw, vw, vp, vp, vw, vp, vp, ctypes.c_size_t, vp, vp]
+    for fn in (lib.rope_spec_init, lib.rope_apply, lib.packed_plan, lib.packed_forward, lib.packed_backward,
+               lib.tree_forward):
+        fn.restype = i
     lib.pyr_selftest_wait.argtypes = [vp, vp]
     lib.pyr_selftest_wait.restype = ctypes.c_int
     lib.pyr_strerror.argtypes = [ctypes.c_int]
@@ -329,6 +377,185 @@ def bsa_backward_noalloc(s: PyrShape, Q, K, V, O, lse, dO, idx, offset, rho, dQ,
                                     (offset, "offset"), (rho, "rho"), (dQ, "dQ"), (dK, "dK"), (dV, "dV"))]
     _check(_L().bsa_backward_noalloc(ctypes.byref(s), *args, _dev(status, "status", True), _stream(stream)),
            "bsa_backward_noalloc")
+
+
+# ---- strided operands: rotary positions, packed prompts, drafted trees ------------------------------------
+
+_DTYPES = {torch.float32: PYR_F32, torch.bfloat16: PYR_BF16}
+
+
+def _dtype_code(dtype):
+    if isinstance(dtype, torch.dtype):
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be float32 or bfloat16, not {dtype}")
+        return _DTYPES[dtype]
+    return int(dtype)
+
+
+def _view(t, name, shape, dtype, device):
+    """PyrView of a tensor [batch, head, row, d] or [head, row, d] of any strides with adjacent elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if _DTYPES.get(t.dtype) != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, which is not the call's")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device than the other operands")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent")
+    return PyrView(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+
+
+def _plain(t, name, dtype, numel, device, nullable=False):
+    """Pointer of a contiguous tensor of one dtype with at least numel elements."""
+    if t is None and nullable:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on another device than the other operands")
+    if not t.is_contiguous() or t.numel() < numel:
+        raise ValueError(f"{name} must be contiguous with at least {numel} elements")
+    return t.data_ptr()
+
+
+def _call(fn, what, device, stream, *args):
+    """fn(*args, stream) with the operands' device current; stream None: that device's current stream."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call(fn, what, device, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    _check(fn(*args, _stream(stream)), what)
+
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_spec(d: int, rot: int = None, base: float = 10000.0, layout: str = "half", scaling: str = None,
+              factor: float = 1.0, trained: int = 0) -> RopeSpec:
+    """Rotary frequencies: the first `rot` elements of a head of d (all by default) turn in pairs (i, i + rot/2)
+    ("half") or (2i, 2i + 1) ("interleaved"), pair i by base^(-2i/rot) radians per position. scaling None,
+    "linear", "ntk" or "yarn" stretches them by `factor` ("yarn" takes the trained length). The result's
+    fields freq (radians per position) and scale may be rewritten for any other schedule."""
+    if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
+    spec = RopeSpec()
+    _check(_L().rope_spec_init(ctypes.byref(spec), int(d), int(d if rot is None else rot), _ROPE_LAYOUTS[layout],
+                               float(base), _ROPE_SCALINGS[scaling], float(factor), int(trained)), "rope_spec")
+    return spec
+
+
+def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inverse: bool = False, status=None,
+               stream=None):
+    """Rotate Q [B, Hq, N, d] into Qo and K [B, Hkv, N, d] into Ko (any strides; in place with Qo is Q, Ko is K;
+    either pair may be None). pos: int32 [B, N] or [N]; None: row n is at pos_offset + n. inverse: the
+    transposed rotation, which turns the outputs' gradients into the inputs'."""
+    first = Q if Q is not None else K
+    if not isinstance(first, torch.Tensor) or first.dim() != 4 or not first.is_cuda:
+        raise TypeError("Q or K must be a CUDA tensor [B, H, N, d]")
+    if (Q is None) != (Qo is None) or (K is None) != (Ko is None):
+        raise ValueError("Q and Qo, and K and Ko, come in pairs")
+    B, _, N, d = first.shape
+    if d != spec.d:
+        raise ValueError(f"the spec is for d = {spec.d}, not {d}")
+    dt, dev = _dtype_code(first.dtype), first.get_device()
+    views, heads = [None] * 4, [0, 0]
+    for i, (x, y, name) in enumerate(((Q, Qo, "Q"), (K, Ko, "K"))):
+        if x is None:
+            continue
+        if x.dim() != 4 or x.shape[1] < 1:
+            raise ValueError(f"{name} must be [B, H, N, d]")
+        heads[i] = x.shape[1]
+        shape = (B, heads[i], N, d)
+        views[i] = _view(x, name, shape, dt, dev)
+        views[2 + i] = _view(y, name + "o", shape, dt, dev)
+    stride = 0
+    if pos is not None:
+        if tuple(pos.shape) not in ((N,), (B, N)):
+            raise ValueError("pos must be [B, N] or [N]")
+        stride = N if pos.dim() == 2 else 0
+    p = _plain(pos, "pos", torch.int32, 0, dev, True)
+    q, k, qo, ko = (None if v is None else ctypes.byref(v) for v in views)
+    _call(_L().rope_apply, "rope_apply", dev, stream, ctypes.byref(spec), B, heads[0], heads[1], N, dt, q, k, p, stride,
+          int(pos_offset), qo, ko, int(bool(inverse)), _plain(status, "status", torch.int32, 1, dev, True))
+
+
+def packed_shape(S: int, T: int, Hq: int, Hkv: int, d: int, dtype) -> PackedShape:
+    """S sequences on a token axis of T tokens (the last sequence may end before T)."""
+    return PackedShape(int(S), int(T), int(Hq), int(Hkv), int(d), _dtype_code(dtype))
+
+
+def packed_plan_elems(s: PackedShape) -> int:
+    return _L().packed_plan_elems(ctypes.byref(s))
+
+
+def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
+    """The work list of sequences [cu[i], cu[i+1]) (int32 CUDA tensor [S + 1]); it serves every packed_forward
+    and packed_backward of this shape and these boundaries. Returns plan (allocated if None)."""
+    dev = cu.get_device() if isinstance(cu, torch.Tensor) else -1
+    c = _plain(cu, "cu", torch.int32, s.S + 1, dev)
+    n = packed_plan_elems(s)
+    if plan is None:
+        plan = torch.empty(max(n, 1), dtype=torch.int32, device=cu.device)
+    _call(_L().packed_plan, "packed_plan", dev, stream, ctypes.byref(s), c,
+          _plain(plan, "plan", torch.int32, n, dev), _plain(status, "status", torch.int32, 1, dev, True))
+    return plan
+
+
+def packed_forward(s: PackedShape, Q, K, V, plan, O, lse=None, status=None, stream=None):
+    """Causal attention inside every packed sequence: Q, O [Hq, T, d], K, V [Hkv, T, d] (any strides), lse fp32
+    [Hq, T]. Tokens outside the sequences are neither used nor written."""
+    dev = Q.get_device() if isinstance(Q, torch.Tensor) else -1
+    q, kv, dt = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d), s.dtype
+    v = [_view(Q, "Q", q, dt, dev), _view(K, "K", kv, dt, dev), _view(V, "V", kv, dt, dev), _view(O, "O", q, dt, dev)]
+    _call(_L().packed_forward, "packed_forward", dev, stream, ctypes.byref(s), *map(ctypes.byref, v[:3]),
+          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), ctypes.byref(v[3]),
+          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev, True),
+          _plain(status, "status", torch.int32, 1, dev, True))
+
+
+def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV, status=None, stream=None):
+    """Gradients of packed_forward for dO, from its O and lse: dQ, dK, dV (views like Q, K, V), with delta an
+    fp32 workspace [Hq, T]."""
+    dev = Q.get_device() if isinstance(Q, torch.Tensor) else -1
+    q, kv, dt = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d), s.dtype
+    v = {n: _view(t, n, sh, dt, dev) for n, t, sh in (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q),
+                                                      ("dO", dO, q), ("dQ", dQ, q), ("dK", dK, kv), ("dV", dV, kv))}
+    r = {n: ctypes.byref(x) for n, x in v.items()}
+    _call(_L().packed_backward, "packed_backward", dev, stream, ctypes.byref(s), r["Q"], r["K"], r["V"],
+          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), r["O"],
+          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev), r["dO"],
+          _plain(delta, "delta", torch.float32, s.Hq * s.T, dev), r["dQ"], r["dK"], r["dV"],
+          _plain(status, "status", torch.int32, 1, dev, True))
+
+
+def tree_shape(B: int, Hq: int, Hkv: int, N: int, T: int, d: int, dtype) -> TreeShape:
+    """T drafted tokens of each of B sequences over caches of N rows."""
+    return TreeShape(int(B), int(Hq), int(Hkv), int(N), int(T), int(d), _dtype_code(dtype))
+
+
+def tree_workspace_bytes(s: TreeShape) -> int:
+    return _L().tree_workspace_bytes(ctypes.byref(s))
+
+
+def tree_forward(s: TreeShape, Q, K, V, lens, parent, O, lse=None, workspace=None, status=None, stream=None):
+    """Attention of drafted tokens: Q, O [B, Hq, T, d], caches K, V [B, Hkv, N, d] (any strides), lens int32 [B]
+    context lengths, parent int32 [B, T] (None: a chain), lse fp32 [B, Hq, T]; the drafted tokens' keys and
+    values are in the cache rows lens[b] + t. workspace: a CUDA uint8 tensor of tree_workspace_bytes(s) bytes."""
+    dev = Q.get_device() if isinstance(Q, torch.Tensor) else -1
+    q, kv, dt = (s.B, s.Hq, s.T, s.d), (s.B, s.Hkv, s.N, s.d), s.dtype
+    v = [_view(Q, "Q", q, dt, dev), _view(K, "K", kv, dt, dev), _view(V, "V", kv, dt, dev), _view(O, "O", q, dt, dev)]
+    w = _plain(workspace, "workspace", torch.uint8, 0, dev)
+    _call(_L().tree_forward, "tree_forward", dev, stream, ctypes.byref(s), *map(ctypes.byref, v[:3]),
+          _plain(lens, "lens", torch.int32, s.B, dev), _plain(parent, "parent", torch.int32, s.B * s.T, dev, True),
+          ctypes.byref(v[3]), _plain(lse, "lse", torch.float32, s.B * s.Hq * s.T, dev, True), w, workspace.numel(),
+          _plain(status, "status", torch.int32, 1, dev, True))
 
 
 def selftest_wait(status, stream=None):

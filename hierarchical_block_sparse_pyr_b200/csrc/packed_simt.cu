@@ -1,0 +1,248 @@
+// Causal attention of packed prompts and its gradients on the CUDA cores, fp32 arithmetic throughout: the
+// fp32 path (reduced-precision tensor-core operands would lose what fp32 callers keep).
+//
+// Forward and dQ: one CTA per (64-row tile, query head), walking the keys up to the tile's end. dK/dV: one
+// CTA per (64-key tile, key/value head), walking the rows from the tile's start on, over the heads of its
+// group, so that every gradient is summed by one CTA in a fixed order. Tiles come longest first from the
+// plan. Rows behind the sequence's end are loaded as zeros, never from memory.
+#include "packed.cuh"
+#include "simt_tile.cuh"
+
+namespace pyr {
+
+namespace {
+
+using namespace simt;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+constexpr int fwd_smem() {
+  return (2 * kTile * (D + 4) + kTile * D) * 4;  // Q, K (P over K), V
+}
+
+// S = Q K^T, online softmax, O += P V over 64-key tiles; P goes over K's buffer.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float *Qs = sm, *Ks = Qs + kTile * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
+  const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
+  if (tile >= a.plan[kListFwd]) return;
+  const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListFwd))[tile];
+  const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float sl2 = rsqrtf((float)D) * kLog2e;
+  const int nrow = min(kTile, end - row0);
+  load_rows<T, D>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  float m[4], l[4], acc[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
+  }
+  const int stop = row0 + nrow;
+  for (int k0 = start; k0 < stop; k0 += kTile) {
+    const int nk = min(kTile, stop - k0);
+    __syncthreads();
+    load_rows<T, D>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<T, D>(Vs, D, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    __syncthreads();
+    float s[4][4];
+    mul_nt<D>(s, Qs, D + 4, Ks, D + 4);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) s[i][j] = k0 + tx + 16 * j <= row0 + 4 * ty + i ? s[i][j] * sl2 : -INFINITY;
+    softmax_step<D>(s, m, l, acc);
+    __syncthreads();  // every thread is done with K
+    store_p(Ps, s);
+    __syncwarp();  // a row of P is written and read by one half-warp
+    mul_acc<D>(acc, Ps, Vs, D);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int t = row0 + 4 * ty + i;
+    if (t >= end) continue;
+    store_row<T, D>(view_at<T>(a.o, 0, h, t), acc[i], 1.f / l[i]);
+    if (a.lse && tx == 0) a.lse[(int64_t)h * g.T + t] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
+  }
+}
+
+// delta[t] = dO_t . O_t for the rows of the sequences; one warp a row
+template <typename T, int D>
+__global__ void __launch_bounds__(256) packed_delta_kernel(PackedGeo g, PackedBwdArgs a) {
+  const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
+  if (tile >= a.plan[kListQ]) return;
+  const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
+  const int lane = threadIdx.x & 31;
+  const int stop = min(w.z + packed_tile_rows(g, kListQ), w.y);
+  constexpr int E = D / 32;
+  for (int t = w.z + (threadIdx.x >> 5); t < stop; t += 8) {
+    const T *o = view_at<T>(a.o, 0, h, t) + lane * E, *d = view_at<T>(a.dout, 0, h, t) + lane * E;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e++) s = fmaf(to_f32(o[e]), to_f32(d[e]), s);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (lane == 0) a.delta[(int64_t)h * g.T + t] = s;
+  }
+}
+
+template <int D>
+constexpr int dq_smem() {
+  return (4 * kTile * (D + 4) + kTile * kPitchP) * 4;  // Q, dO, K, V, dS
+}
+
+// dS = P (dO V^T - delta), dQ += dS K
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, PackedBwdArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int P = D + 4;
+  float *Qs = sm, *Gs = Qs + kTile * P, *Ks = Gs + kTile * P, *Vs = Ks + kTile * P, *Ps = Vs + kTile * P;
+  const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
+  if (tile >= a.plan[kListQ]) return;
+  const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
+  const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
+  const int nrow = min(kTile, end - row0);
+  load_rows<T, D>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<T, D>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
+  float lse2[4], del[4], acc[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int t = min(row0 + 4 * ty + i, end - 1);
+    lse2[i] = a.lse[(int64_t)h * g.T + t] * kLog2e;
+    del[i] = a.delta[(int64_t)h * g.T + t];
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
+  }
+  const int stop = row0 + nrow;
+  for (int k0 = start; k0 < stop; k0 += kTile) {
+    const int nk = min(kTile, stop - k0);
+    __syncthreads();
+    load_rows<T, D>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<T, D>(Vs, P, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    mul_nt<D>(s, Qs, P, Ks, P);
+    mul_nt<D>(dp, Gs, P, Vs, P);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        s[i][j] = k0 + tx + 16 * j <= row0 + 4 * ty + i ? exp2f(s[i][j] * sl2 - lse2[i]) * (dp[i][j] - del[i]) : 0.f;
+    __syncwarp();
+    store_p(Ps, s);
+    __syncwarp();
+    mul_acc<D>(acc, Ps, Ks, P);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    if (row0 + 4 * ty + i < end) store_row<T, D>(view_at<T>(a.dq, 0, h, row0 + 4 * ty + i), acc[i], scale);
+}
+
+// rows = keys, columns = queries: dV += P^T dO, dK += dS^T Q over the rows of the group's heads
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g, PackedBwdArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int P = D + 4;
+  float *Ks = sm, *Vs = Ks + kTile * P, *Qs = Vs + kTile * P, *Gs = Qs + kTile * P, *Ps = Gs + kTile * P;
+  const int tile = blockIdx.x / g.Hkv, hk = blockIdx.x - tile * g.Hkv;
+  if (tile >= a.plan[kListK]) return;
+  const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListK))[tile];
+  const int end = w.y, key0 = w.z;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
+  const int nk = min(kTile, end - key0);
+  load_rows<T, D>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
+  load_rows<T, D>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
+  float dk[4][D / 16], dv[4][D / 16];
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) dk[i][c] = dv[i][c] = 0.f;
+  for (int h = hk * g.G; h < (hk + 1) * g.G; h++) {
+    for (int q0 = key0; q0 < end; q0 += kTile) {
+      const int nq = min(kTile, end - q0);
+      __syncthreads();
+      load_rows<T, D>(Qs, P, view_at<T>(a.q, 0, h, q0), a.q.row, nq);
+      load_rows<T, D>(Gs, P, view_at<T>(a.dout, 0, h, q0), a.dout.row, nq);
+      __syncthreads();
+      float s[4][4], dp[4][4];
+      mul_nt<D>(s, Ks, P, Qs, P);
+      mul_nt<D>(dp, Vs, P, Gs, P);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int t = q0 + tx + 16 * j, tc = min(t, end - 1);
+        const float lse2 = a.lse[(int64_t)h * g.T + tc] * kLog2e, del = a.delta[(int64_t)h * g.T + tc];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          s[i][j] = key0 + 4 * ty + i <= t && t < end ? exp2f(s[i][j] * sl2 - lse2) : 0.f;
+          dp[i][j] = s[i][j] * (dp[i][j] - del);
+        }
+      }
+      store_p(Ps, s);
+      __syncwarp();
+      mul_acc<D>(dv, Ps, Gs, P);
+      __syncwarp();
+      store_p(Ps, dp);
+      __syncwarp();
+      mul_acc<D>(dk, Ps, Qs, P);
+      __syncwarp();
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (4 * ty + i >= nk) continue;
+    store_row<T, D>(view_at<T>(a.dk, 0, hk, key0 + 4 * ty + i), dk[i], scale);
+    store_row<T, D>(view_at<T>(a.dv, 0, hk, key0 + 4 * ty + i), dv[i], 1.f);
+  }
+}
+
+template <typename K, typename A>
+cudaError_t launch(K kern, int64_t blocks, int threads, int smem, const PackedGeo& g, const A& a, cudaStream_t st) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<(unsigned)blocks, threads, smem, st>>>(g, a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_bwd(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
+  const cudaError_t e = launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads,
+                               dq_smem<D>(), g, a, st);
+  if (e != cudaSuccess) return e;
+  return launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads, dq_smem<D>(), g, a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_fwd_simt(const PackedGeo& g, const PackedFwdArgs& a, cudaStream_t st) {
+  const int64_t blocks = packed_list_cap(g, kListFwd) * g.Hq;
+  if (g.dtype == PYR_F32)
+    return g.d == 64 ? launch(packed_fwd_simt_kernel<float, 64>, blocks, kThreads, fwd_smem<64>(), g, a, st)
+                     : launch(packed_fwd_simt_kernel<float, 128>, blocks, kThreads, fwd_smem<128>(), g, a, st);
+  return g.d == 64 ? launch(packed_fwd_simt_kernel<__nv_bfloat16, 64>, blocks, kThreads, fwd_smem<64>(), g, a, st)
+                   : launch(packed_fwd_simt_kernel<__nv_bfloat16, 128>, blocks, kThreads, fwd_smem<128>(), g, a, st);
+}
+
+cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
+  const int64_t blocks = packed_list_cap(g, kListQ) * g.Hq;
+  if (g.dtype == PYR_F32)
+    return g.d == 64 ? launch(packed_delta_kernel<float, 64>, blocks, 256, 0, g, a, st)
+                     : launch(packed_delta_kernel<float, 128>, blocks, 256, 0, g, a, st);
+  return g.d == 64 ? launch(packed_delta_kernel<__nv_bfloat16, 64>, blocks, 256, 0, g, a, st)
+                   : launch(packed_delta_kernel<__nv_bfloat16, 128>, blocks, 256, 0, g, a, st);
+}
+
+cudaError_t launch_packed_bwd_simt(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
+  if (g.dtype == PYR_F32) return g.d == 64 ? launch_bwd<float, 64>(g, a, st) : launch_bwd<float, 128>(g, a, st);
+  return g.d == 64 ? launch_bwd<__nv_bfloat16, 64>(g, a, st) : launch_bwd<__nv_bfloat16, 128>(g, a, st);
+}
+
+}  // namespace pyr

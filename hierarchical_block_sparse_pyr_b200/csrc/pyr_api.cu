@@ -324,6 +324,7 @@ const char* pyr_strerror(int code) {
     case PYR_ECUDA: return "CUDA launch failed";
     case PYR_ETIMEOUT: return "a bounded device wait ran out";
     case PYR_EBADIDX: return "idx lists a block that is not strictly before its query block, or not ascending";
+    case PYR_EBADSEQ: return "sequence boundaries, lengths or tree parents out of order or out of range";
     default: return "unknown status";
   }
 }

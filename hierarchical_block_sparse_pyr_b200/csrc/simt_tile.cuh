@@ -1,0 +1,153 @@
+// 64 x 64 tiles of fp32 attention on the CUDA cores, 256 threads. Thread (tx, ty) = (tid % 16, tid / 16)
+// owns rows 4 ty .. 4 ty + 3 of every product; of a 64 x 64 product it owns the columns tx + 16 j (four,
+// which keeps the 16-byte reads of the other operand's rows conflict-free with a row pitch of D + 4), of a
+// 64 x D product the columns 4 tx + 64 j .. + 3.
+#pragma once
+
+#include "view.cuh"
+
+namespace pyr {
+namespace simt {
+
+constexpr int kTile = 64;
+constexpr int kThreads = 256;
+constexpr int kPitchP = kTile + 4;
+
+// dst[r][0 .. D) = row r of src where wanted(r), zeros in the other of the 64 rows
+template <typename T, int D, typename F>
+__device__ __forceinline__ void load_rows_if(float* dst, int pitch, const T* src, int64_t stride, F wanted) {
+  constexpr int E = 16 / sizeof(T), C = D / E;
+  for (int x = threadIdx.x; x < kTile * C; x += kThreads) {
+    const int r = x / C, c = x - r * C;
+    float* d = dst + r * pitch + c * E;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (wanted(r)) v = *reinterpret_cast<const uint4*>(src + r * stride + c * E);
+    if (sizeof(T) == 4) {
+      *reinterpret_cast<uint4*>(d) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        d[2 * i] = __uint_as_float(w[i] << 16);
+        d[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void load_rows(float* dst, int pitch, const T* src, int64_t stride, int n) {
+  load_rows_if<T, D>(dst, pitch, src, stride, [n](int r) { return r < n; });
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j] over D elements
+template <int D>
+__device__ __forceinline__ void mul_nt(float (&acc)[4][4], const float* A, int pa, const float* B, int pb) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int e = 0; e < D; e += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * pa + e);
+#pragma unroll
+    for (int j = 0; j < 4; j++) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * pb + e);
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+      }
+  }
+}
+
+// acc[i][4 j + c] += sum_k P[4 ty + i][k] V[k][4 tx + 64 j + c], k = 0 .. 63
+template <int D>
+__device__ __forceinline__ void mul_acc(float (&acc)[4][D / 16], const float* P, const float* V, int pv) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll 2
+  for (int k = 0; k < kTile; k += 4) {
+    float p[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float4 x = *reinterpret_cast<const float4*>(P + (4 * ty + i) * kPitchP + k);
+      p[i][0] = x.x, p[i][1] = x.y, p[i][2] = x.z, p[i][3] = x.w;
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; kk++)
+#pragma unroll
+      for (int j = 0; j < D / 64; j++) {
+        const float4 v = *reinterpret_cast<const float4*>(V + (k + kk) * pv + 4 * tx + 64 * j);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          acc[i][4 * j + 0] = fmaf(p[i][kk], v.x, acc[i][4 * j + 0]);
+          acc[i][4 * j + 1] = fmaf(p[i][kk], v.y, acc[i][4 * j + 1]);
+          acc[i][4 * j + 2] = fmaf(p[i][kk], v.z, acc[i][4 * j + 2]);
+          acc[i][4 * j + 3] = fmaf(p[i][kk], v.w, acc[i][4 * j + 3]);
+        }
+      }
+  }
+}
+
+__device__ __forceinline__ void store_p(float* P, const float (&s)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) P[(4 * ty + i) * kPitchP + tx + 16 * j] = s[i][j];
+}
+
+// one step of the online softmax over a 64-column tile of scores in log2 units (-inf: not attended):
+// s becomes the probabilities against the new maximum, acc is rescaled
+template <int D>
+__device__ __forceinline__ void softmax_step(float (&s)[4][4], float (&m)[4], float (&l)[4],
+                                             float (&acc)[4][D / 16]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
+    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(m[i], mx);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float f = exp2f(m[i] - mu);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      s[i][j] = exp2f(s[i][j] - mu);
+      sum += s[i][j];
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l[i] = l[i] * f + sum;
+    m[i] = mn;
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) acc[i][c] *= f;
+  }
+}
+
+// row 4 ty + i of a 64 x D accumulator, times f, to a row of T
+template <typename T, int D>
+__device__ __forceinline__ void store_row(T* dst, const float (&acc)[D / 16], float f) {
+  const int tx = threadIdx.x & 15;
+#pragma unroll
+  for (int j = 0; j < D / 64; j++) {
+    const float x[4] = {acc[4 * j] * f, acc[4 * j + 1] * f, acc[4 * j + 2] * f, acc[4 * j + 3] * f};
+    if (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(dst) + 4 * tx + 64 * j) =
+          make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+      __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+      uint2 u = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(dst) + 4 * tx + 64 * j) = u;
+    }
+  }
+}
+
+}  // namespace simt
+}  // namespace pyr

@@ -1,0 +1,138 @@
+// Drafted trees over a cache: the C entry point and the kernel that joins the parts.
+#include "tree.cuh"
+
+namespace pyr {
+
+namespace {
+
+constexpr int kJoinWarps = 8;
+
+// One warp a row: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of the row's segment in
+// stream order. Segments that one CTA held whole were written by it.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, TreeArgs a) {
+  extern __shared__ int s_pre[];
+  __shared__ int warp_sums[32];
+  tree_prefix(g, a, s_pre, warp_sums);
+  const TreeStream ts(g, s_pre);
+  const int b = blockIdx.x / ts.HR, hr = blockIdx.x - b * ts.HR;
+  const int64_t nt = s_pre[b + 1] - s_pre[b], first = (int64_t)s_pre[b] * ts.HR + hr * nt;
+  // first and last CTA of the segment
+  int c0 = (int)(first * ts.C / ts.total), c1 = (int)((first + nt - 1) * ts.C / ts.total);
+  while (c0 > 0 && ts.cut(c0) > first) c0--;
+  while (ts.cut(c0 + 1) <= first) c0++;
+  while (c1 > 0 && ts.cut(c1) > first + nt - 1) c1--;
+  while (ts.cut(c1 + 1) <= first + nt - 1) c1++;
+  if (c0 == c1) return;
+  const int slot0 = ts.cut(c0) < first ? 1 : 0;  // the first CTA may hold another segment's end before it
+  const int hk = hr / g.RG, rg = hr - hk * g.RG;
+  const int rr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int r = rg * g.RR + rr;
+  if (rr >= g.RR || r >= g.rows) return;
+  const int n = c1 - c0 + 1;
+  auto part = [&](int i) { return (int64_t)((c0 + i) * 2 + (i == 0 ? slot0 : 0)) * g.RR + rr; };
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_ml[2 * part(i)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float mu = m == -INFINITY ? 0.f : m;
+  constexpr int E = D / 32;
+  float acc[E] = {}, l = 0.f;
+  for (int base = 0; base < n; base += 32) {
+    float w = 0.f;
+    if (base + lane < n) {
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * part(base + lane));
+      w = exp2f(ml.x - mu);
+      l += w * ml.y;
+    }
+    const int cnt = min(32, n - base);
+#pragma unroll 4
+    for (int i = 0; i < cnt; i++) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* p = a.part_o + part(base + i) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e++) acc[e] = fmaf(wi, p[e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const int h = hk * g.G + r / g.T, t = r % g.T;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  T* dst = view_at<T>(a.o, b, h, t) + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e++) dst[e] = (T)(acc[e] * inv);
+  if (a.lse && lane == 0)
+    a.lse[((int64_t)b * g.Hq + h) * g.T + t] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <typename T, int D>
+cudaError_t launch_join(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
+  const int rows = g.rows < g.RR ? g.rows : g.RR;
+  const dim3 grid(g.B * g.Hkv * g.RG, (rows + kJoinWarps - 1) / kJoinWarps);
+  tree_join_kernel<T, D><<<grid, kJoinWarps * 32, (g.B + 1) * sizeof(int), st>>>(g, a);
+  return cudaGetLastError();
+}
+
+int make_tree_geo(const tree_shape* s, TreeGeo* g) {
+  if (!s || s->B <= 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Hq % s->Hkv || s->T <= 0 || s->N < s->T) return PYR_EINVAL;
+  if (s->dtype != PYR_F32 && s->dtype != PYR_BF16) return PYR_EUNSUPPORTED;
+  if (s->d != 64 && s->d != 128) return PYR_EUNSUPPORTED;
+  if (s->T > kTreeMaxT || s->B > 4096 || s->Hq > 65535 || s->N > (1 << 28)) return PYR_EUNSUPPORTED;
+  TreeGeo t = {s->B, s->Hq, s->Hkv, s->Hq / s->Hkv, s->N, s->T, s->d, s->dtype};
+  t.rows = t.G * t.T;
+  t.RR = 64;
+  t.BK = 64;
+  t.C = 296;
+  t.RG = (t.rows + t.RR - 1) / t.RR;
+  if ((int64_t)t.B * (((int64_t)t.N + t.BK - 1) / t.BK) > 0x7fffffff ||
+      (int64_t)t.B * t.Hkv * t.RG > 0x7fffffff)
+    return PYR_EUNSUPPORTED;
+  *g = t;
+  return PYR_OK;
+}
+
+size_t tree_part_rows(const TreeGeo& g) { return (size_t)g.C * 2 * g.RR; }
+
+}  // namespace
+
+cudaError_t launch_tree_join(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
+  if (g.dtype == PYR_F32) return g.d == 64 ? launch_join<float, 64>(g, a, st) : launch_join<float, 128>(g, a, st);
+  return g.d == 64 ? launch_join<__nv_bfloat16, 64>(g, a, st) : launch_join<__nv_bfloat16, 128>(g, a, st);
+}
+
+}  // namespace pyr
+
+extern "C" {
+
+size_t tree_workspace_bytes(const tree_shape* s) {
+  pyr::TreeGeo g;
+  return pyr::make_tree_geo(s, &g) == PYR_OK ? pyr::tree_part_rows(g) * (g.d + 2) * sizeof(float) : 0;
+}
+
+int tree_forward(const tree_shape* s, const pyr_view* Q, const pyr_view* K, const pyr_view* V, const int32_t* len,
+                 const int32_t* parent, const pyr_view* O, float* lse, void* workspace, size_t workspace_bytes,
+                 int* dev_status, void* stream) {
+  pyr::TreeGeo g;
+  const int rc = pyr::make_tree_geo(s, &g);
+  if (rc) return rc;
+  pyr::TreeArgs a;
+  if (!pyr::check_view(Q, g.B, g.Hq, g.T, g.d, g.dtype, false, &a.q) ||
+      !pyr::check_view(K, g.B, g.Hkv, g.N, g.d, g.dtype, false, &a.k) ||
+      !pyr::check_view(V, g.B, g.Hkv, g.N, g.d, g.dtype, false, &a.v) ||
+      !pyr::check_view(O, g.B, g.Hq, g.T, g.d, g.dtype, true, &a.o) || !len || !workspace || !pyr::aligned4(len) ||
+      !pyr::aligned4(parent) || !pyr::aligned4(lse) || !pyr::aligned16(workspace) ||
+      workspace_bytes < tree_workspace_bytes(s))
+    return PYR_EINVAL;
+  a.len = len;
+  a.parent = parent;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = a.part_o + pyr::tree_part_rows(g) * g.d;
+  a.status = dev_status;
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = pyr::launch_tree_simt(g, a, st);
+  if (e == cudaSuccess) e = pyr::launch_tree_join(g, a, st);
+  return e == cudaSuccess ? PYR_OK : PYR_ECUDA;
+}
+
+}  // extern "C"

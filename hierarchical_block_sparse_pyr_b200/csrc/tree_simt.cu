@@ -1,0 +1,122 @@
+// Attention of drafted trees over a cache on the CUDA cores, fp32 arithmetic: 64 rows x 64 keys a step.
+// Every CTA walks its share of the stream of tiles (tree.cuh) and writes the rows of a segment itself where
+// it holds the whole segment, else a part for the join.
+#include "simt_tile.cuh"
+#include "tree.cuh"
+
+namespace pyr {
+
+namespace {
+
+using namespace simt;
+
+template <int D>
+constexpr int tree_smem() {
+  return (2 * kTile * (D + 4) + kTile * D) * 4;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float *Qs = sm, *Ks = Qs + kTile * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
+  int* pre = reinterpret_cast<int*>(Vs + kTile * D);
+  __shared__ int warp_sums[32];
+  __shared__ TreeMaskBuf masks;
+  tree_prefix(g, a, pre, warp_sums);
+  const TreeStream ts(g, pre);
+  if (blockIdx.x >= ts.C) return;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
+  const int64_t x0 = ts.cut(blockIdx.x), x1 = ts.cut(blockIdx.x + 1);
+  for (int64_t x = x0; x < x1;) {
+    int b, hr, tiles, len;
+    int64_t first;
+    ts.find(x, &b, &hr, &first, &tiles);
+    const int t0 = (int)(x - first), t1 = (int)(x1 - first < tiles ? x1 - first : tiles);
+    const int hk = hr / g.RG, r0 = (hr - hk * g.RG) * g.RR;
+    const bool good = tree_len(g, a, b, &len);
+    if (!good) len = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) tree_masks(g, a, b, good, &masks);
+    const int nr = min(kTile, g.rows - r0);
+    for (int i = threadIdx.x; i < kTile * (D / 8); i += kThreads) {
+      const int r = i / (D / 8), c = i - r * (D / 8), ra = r0 + r;
+      const T* src = r < nr ? view_at<T>(a.q, b, hk * g.G + ra / g.T, ra % g.T) + c * 8 : nullptr;
+#pragma unroll
+      for (int e = 0; e < 8; e++) Qs[r * (D + 4) + c * 8 + e] = src ? to_f32(src[e]) : 0.f;
+    }
+    __syncthreads();
+    const unsigned long long used = tree_used(&masks);
+    float m[4], l[4], acc[4][D / 16];
+    unsigned long long mask[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      const int r = 4 * ty + i;
+      mask[i] = r < nr ? masks.mask[(r0 + r) % g.T] : 0ull;
+#pragma unroll
+      for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
+    }
+    for (int t = t0; t < t1; t++) {
+      const int k0 = t * kTile;
+      auto wanted = [&](int r) {
+        const int u = k0 + r - len;
+        return good && (u < 0 || (u < g.T && ((used >> u) & 1)));
+      };
+      __syncthreads();
+      load_rows_if<T, D>(Ks, D + 4, view_at<T>(a.k, b, hk, k0), a.k.row, wanted);
+      load_rows_if<T, D>(Vs, D, view_at<T>(a.v, b, hk, k0), a.v.row, wanted);
+      __syncthreads();
+      float s[4][4];
+      mul_nt<D>(s, Qs, D + 4, Ks, D + 4);
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          s[i][j] = tree_sees(k0 + tx + 16 * j, len, mask[i]) && good ? s[i][j] * sl2 : -INFINITY;
+      softmax_step<D>(s, m, l, acc);
+      __syncthreads();
+      store_p(Ps, s);
+      __syncwarp();
+      mul_acc<D>(acc, Ps, Vs, D);
+    }
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int64_t part = (int64_t)(blockIdx.x * 2 + (x == x0 ? 0 : 1)) * g.RR;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int r = 4 * ty + i;
+      if (r >= nr) continue;
+      if (whole) {
+        const int h = hk * g.G + (r0 + r) / g.T, t = (r0 + r) % g.T;
+        store_row<T, D>(view_at<T>(a.o, b, h, t), acc[i], l[i] > 0.f ? 1.f / l[i] : 0.f);
+        if (a.lse && tx == 0)
+          a.lse[((int64_t)b * g.Hq + h) * g.T + t] =
+              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+      } else {
+        store_row<float, D>(a.part_o + (part + r) * D, acc[i], 1.f);
+        if (tx == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (part + r)) = make_float2(m[i], l[i]);
+      }
+    }
+    x = first + t1;
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
+  auto kern = tree_simt_kernel<T, D>;
+  const int smem = tree_smem<D>() + (g.B + 1) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<g.C, kThreads, smem, st>>>(g, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_simt(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
+  if (g.dtype == PYR_F32) return g.d == 64 ? launch<float, 64>(g, a, st) : launch<float, 128>(g, a, st);
+  return g.d == 64 ? launch<__nv_bfloat16, 64>(g, a, st) : launch<__nv_bfloat16, 128>(g, a, st);
+}
+
+}  // namespace pyr

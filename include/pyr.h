@@ -76,6 +76,7 @@ extern "C" {
 #define PYR_ECUDA 3        /* the CUDA runtime refused a launch */
 #define PYR_ETIMEOUT 4     /* device: a bounded wait ran out (kernel returned early) */
 #define PYR_EBADIDX 5      /* device: idx held a block that is not strictly before its query block */
+#define PYR_EBADSEQ 6      /* device: sequence boundaries, lengths or tree parents out of order or out of range */
 
 #define PYR_F32 0
 #define PYR_BF16 1
@@ -435,6 +436,187 @@ PYR_API int bsa_backward(const pyr_shape* s, const void* Q, const void* K, const
 PYR_API int bsa_backward_noalloc(const pyr_shape* s, const void* Q, const void* K, const void* V, const void* O,
                                  const float* lse, const void* dO, const int32_t* idx, const int32_t* offset,
                                  const int32_t* rho, void* dQ, void* dK, void* dV, int* dev_status, void* stream);
+
+/*
+ * Strided operands of the entry points below. A pyr_view is a tensor
+ * [batch][head][row][d] whose d elements of a row are adjacent; the strides
+ * count elements. Head-major [B][H][N][d] and token-major [B][N][H][d] (or
+ * [T][H][d]) memory are both views. `data` is 16-byte aligned, and the stride
+ * of every axis of more than one entry is a multiple of 16 bytes and at least
+ * d; the rows of a view that is written must not overlap. PYR_EINVAL
+ * otherwise.
+ */
+typedef struct pyr_view {
+  void* data;    /* device */
+  int64_t batch; /* elements between batches (ignored where there is one batch) */
+  int64_t head;  /* elements between heads */
+  int64_t row;   /* elements between rows (positions, tokens) */
+} pyr_view;
+
+/*
+ * Rotary positions. The pages rotate queries and keys before routing and token
+ * attention and score the prefix states with the un-rotated ones (PHBA
+ * summary, 3.1, 3.3, A.1.2); rope_apply makes the one from the other.
+ * Pair i of a head's first `rot` elements, (x_i, x_{i + rot/2}) for ROPE_HALF
+ * or (x_{2i}, x_{2i+1}) for ROPE_INTERLEAVED, at position p becomes
+ *   scale * (a cos w - b sin w, a sin w + b cos w),   w = p * freq[i],
+ * and elements rot .. d-1 are passed through.
+ */
+#define ROPE_HALF 0
+#define ROPE_INTERLEAVED 1
+
+#define ROPE_SCALE_NONE 0
+#define ROPE_SCALE_LINEAR 1 /* positions divided by factor */
+#define ROPE_SCALE_NTK 2    /* base * factor^(rot / (rot - 2)): the slowest pair is slowed by factor, the fastest not */
+#define ROPE_SCALE_YARN 3   /* per pair between unscaled (>= 32 turns over the trained length) and linear (<= 1 turn),
+                               a ramp over the pair index between; scale = 0.1 ln(factor) + 1 */
+
+typedef struct rope_spec {
+  int d;           /* head dimension, 64 or 128 */
+  int rot;         /* rotated elements of a head: even, 2 .. d */
+  int layout;      /* ROPE_HALF or ROPE_INTERLEAVED */
+  int reserved;    /* 0 */
+  double scale;    /* factor on the rotated elements (1: a pure rotation) */
+  double freq[64]; /* radians per position of pair 0 .. rot/2 - 1 */
+} rope_spec;
+
+/*
+ * rope_spec_init - fill a rope_spec on the host: freq[i] = base^(-2i/rot),
+ * scaled for contexts longer than the trained one as `scaling` says (factor
+ * >= 1, `trained` the trained length, read by ROPE_SCALE_YARN only). A caller
+ * with another schedule writes freq and scale itself.
+ * PYR_EINVAL: a NULL spec, an odd or out-of-range rot, an unknown layout or
+ * scaling, base or factor not finite, base <= 1 or factor < 1 where a scaling
+ * is asked for, trained < 1 or rot < 4 where the scaling needs them.
+ */
+PYR_API int rope_spec_init(rope_spec* spec, int d, int rot, int layout, double base, int scaling, double factor,
+                           int trained);
+
+/*
+ * rope_apply - rotate queries and keys.
+ *   Q, Qo  views [B][Hq][N][d] (Q read, Qo written), or both NULL with Hq 0.
+ *   K, Ko  views [B][Hkv][N][d], or both NULL with Hkv 0.
+ *          Qo may be Q itself and Ko may be K itself (same data and strides);
+ *          any other overlap is not allowed.
+ *   pos    device int32: row n of batch b sits at position
+ *          pos[b * pos_stride + n] (pos_stride 0: shared by the batches), or
+ *          NULL: at pos_offset + n. Any int32 value is a position.
+ *   inverse 0: rotate; otherwise the transposed map (the angle negated, the
+ *          same scale), which is the gradient: dQ = inverse(dQo).
+ * Angles are taken in double and reduced to a fraction of a turn before
+ * sine and cosine, so far positions keep their accuracy; the products are
+ * fp32, rounded once to the dtype (PYR_F32 or PYR_BF16).
+ */
+PYR_API int rope_apply(const rope_spec* spec, int B, int Hq, int Hkv, int N, int dtype, const pyr_view* Q,
+                       const pyr_view* K, const int32_t* pos, int64_t pos_stride, int pos_offset, const pyr_view* Qo,
+                       const pyr_view* Ko, int inverse, int* dev_status, void* stream);
+
+/*
+ * Packed prompts: causal attention over whole sequences of different lengths
+ * laid one after another on one token axis (PHBA summary, A.1.1 and A.1.2, name
+ * packed sequences with their boundaries). Sequence s holds the tokens
+ * [cu[s], cu[s+1]) of the axis; a token attends to itself and to the earlier
+ * tokens of its sequence, with softmax scale 1/sqrt(d). Sequences may be
+ * empty. Tokens outside every sequence (before cu[0], or behind cu[S]) belong
+ * to the caller: nothing of them is used and their outputs are left as they
+ * were. The values inside the sequences are taken to be finite.
+ */
+typedef struct packed_shape {
+  int S;     /* sequences, >= 1 */
+  int T;     /* tokens on the axis, >= 1 (cu[S] <= T) */
+  int Hq;    /* query heads */
+  int Hkv;   /* key/value heads; Hq % Hkv == 0 */
+  int d;     /* 64 or 128 */
+  int dtype; /* PYR_F32 or PYR_BF16 */
+} packed_shape;
+
+/* int32 elements of a plan; 0 on a bad shape. */
+PYR_API size_t packed_plan_elems(const packed_shape* s);
+
+/*
+ * packed_plan - the work list of a packed batch, longest tiles first, made on
+ * the device from the boundaries. One plan serves every forward and backward
+ * call of the same shape and boundaries (every layer of a model).
+ *   cu    device int32 [S + 1]: 0 <= cu[0] <= cu[1] <= ... <= cu[S] <= T. If
+ *         the values break this, the plan lists no work and PYR_EBADSEQ is
+ *         reported in *dev_status.
+ *   plan  device int32 [packed_plan_elems], 16-byte aligned (written).
+ */
+PYR_API int packed_plan(const packed_shape* s, const int32_t* cu, int32_t* plan, int* dev_status, void* stream);
+
+/*
+ * packed_forward - causal attention of every sequence of the batch.
+ *   Q, O   views [Hq][T][d]; K, V views [Hkv][T][d] (batch strides ignored).
+ *   plan   device, as written by packed_plan for the same shape.
+ *   lse    device fp32 [Hq][T] or NULL (written): natural log-sum-exp.
+ * bf16 runs on the tcgen05 tensor cores with fp32 statistics and accumulators
+ * (probabilities are rounded to bf16 for the second product); fp32 runs in
+ * fp32 on the CUDA cores.
+ */
+PYR_API int packed_forward(const packed_shape* s, const pyr_view* Q, const pyr_view* K, const pyr_view* V,
+                           const int32_t* plan, const pyr_view* O, float* lse, int* dev_status, void* stream);
+
+/*
+ * packed_backward - gradients of packed_forward for the output gradient dO:
+ *   P = exp(q . k / sqrt(d) - lse), D = dO . O, dS = P (dO . v - D),
+ *   dQ = sum_k dS k / sqrt(d), dK = sum_t dS q / sqrt(d), dV = sum_t P dO,
+ * t running over the rows of all heads of the key's group.
+ *   Q, K, V, O, dO views as above; O and lse as written by packed_forward.
+ *   delta  device fp32 [Hq][T] workspace (overwritten with D).
+ *   dQ     view [Hq][T][d]; dK, dV views [Hkv][T][d] (written; no overlap with
+ *          any other operand).
+ * Every gradient element is summed by one thread block in a fixed order, in
+ * fp32: the result does not depend on timing.
+ */
+PYR_API int packed_backward(const packed_shape* s, const pyr_view* Q, const pyr_view* K, const pyr_view* V,
+                            const int32_t* plan, const pyr_view* O, const float* lse, const pyr_view* dO, float* delta,
+                            const pyr_view* dQ, const pyr_view* dK, const pyr_view* dV, int* dev_status, void* stream);
+
+/*
+ * Drafted trees over a cache: T tokens of each sequence attend to the
+ * sequence's cached keys and to their own ancestors among the T (one token:
+ * plain decode with a length of its own per sequence). The keys and values of
+ * the drafted tokens are already in the cache, behind the context.
+ */
+#define PYR_TREE_ROOT (-1)   /* parent of a token that follows the context directly */
+#define PYR_TREE_ABSENT (-2) /* the slot holds no token */
+
+typedef struct tree_shape {
+  int B;     /* sequences, 1 .. 4096 */
+  int Hq;    /* query heads */
+  int Hkv;   /* key/value heads; Hq % Hkv == 0 */
+  int N;     /* rows of the cache */
+  int T;     /* drafted tokens per sequence, 1 .. 64 */
+  int d;     /* 64 or 128 */
+  int dtype; /* PYR_F32 or PYR_BF16 */
+} tree_shape;
+
+/* Device workspace bytes of tree_forward; 0 on a bad shape. */
+PYR_API size_t tree_workspace_bytes(const tree_shape* s);
+
+/*
+ * tree_forward - attention of the drafted tokens, softmax scale 1/sqrt(d).
+ *   Q, O   views [B][Hq][T][d]; K, V views [B][Hkv][N][d].
+ *   len    device int32 [B]: cached context tokens, 0 <= len[b] and
+ *          len[b] + T <= N. Drafted token t of sequence b has its key and value
+ *          in row len[b] + t. A length out of range makes every slot of its
+ *          sequence absent and reports PYR_EBADSEQ in *dev_status.
+ *   parent device int32 [B][T] or NULL (a chain: parent[t] = t - 1):
+ *          0 <= parent[t] < t, or PYR_TREE_ROOT, or PYR_TREE_ABSENT. Any
+ *          other value makes the slot absent and reports PYR_EBADSEQ. A token
+ *          below an absent one is absent.
+ *   O, lse (lse fp32 [B][Hq][T] or NULL) written; absent slots get O = 0 and
+ *          lse = -inf, and the cache rows of absent slots are not used.
+ *   workspace device, 16-byte aligned, >= tree_workspace_bytes bytes; calls
+ *          that share one must be ordered on a stream.
+ * Cache rows at or behind len[b] + T are not used. The cache is read once per
+ * key/value head for up to 256 query rows (T tokens of Hq / Hkv heads); the
+ * work is split evenly over the GPU along the cached tokens and the parts are
+ * joined in a fixed order.
+ */
+PYR_API int tree_forward(const tree_shape* s, const pyr_view* Q, const pyr_view* K, const pyr_view* V,
+                         const int32_t* len, const int32_t* parent, const pyr_view* O, float* lse, void* workspace,
+                         size_t workspace_bytes, int* dev_status, void* stream);
 
 /*
  * pyr_selftest_wait - exercise the bounded waits the kernels rely on: one

@@ -1,0 +1,199 @@
+"""Packed prompts on the GPU against the definition in double.
+
+Tolerances. fp32: scores are d products accumulated in fp32 (error <= d 2^-24 |q||k|/sqrt(d), a few 1e-6
+here), so 2e-5 relative to the row's largest |v| for O, 2e-5 for lse and 1e-4 of the tensor's largest
+element for the gradients. bf16: the inputs are exact; P (forward), P and dS (backward) are rounded to bf16
+once (2^-8 relative each, averaging over the keys), and the outputs are rounded once (2^-8): max-abs error
+<= 2^-8 |x| + 2^-7 max over the row's keys of |v| for O; for the gradients relative L2 <= 3 * 2^-8 and
+max-abs <= 2^-5 of the largest element; D comes from a bf16 O.
+"""
+import pytest
+import torch
+
+import _plain64 as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _tensor(order, H, T, d, dtype, g):
+    x = torch.randn((H, T, d), generator=g).to(dtype).cuda()
+    return x if order == "hnd" else x.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+def _batch(lens, pad, Hq, Hkv, d, dtype, order, seed, lead=0):
+    g = torch.Generator().manual_seed(seed)
+    cu = [lead]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T = cu[-1] + pad
+    Q, dO = _tensor(order, Hq, T, d, dtype, g), _tensor(order, Hq, T, d, dtype, g)
+    K, V = _tensor(order, Hkv, T, d, dtype, g), _tensor(order, Hkv, T, d, dtype, g)
+    # tokens of no sequence hold NaN: they must never be used
+    for x in (Q, K, V, dO):
+        x[:, :lead] = float("nan")
+        x[:, cu[-1]:] = float("nan")
+    return cu, T, Q, K, V, dO
+
+
+def _forward(P, cu, T, Q, K, V, fill=7.0):
+    s = P.packed_shape(len(cu) - 1, T, Q.shape[0], K.shape[0], Q.shape[2], Q.dtype)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plan = P.packed_plan(s, torch.tensor(cu, dtype=torch.int32, device="cuda"), status=status)
+    O = torch.full_like(Q, fill)
+    lse = torch.full((Q.shape[0], T), fill, device="cuda")
+    P.packed_forward(s, Q, K, V, plan, O, lse, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    return s, plan, O, lse
+
+
+CASES = [
+    # lens, pad, lead, Hq, Hkv, d, dtype, order
+    ([1], 0, 0, 1, 1, 64, F32, "hnd"),
+    ([1], 0, 0, 2, 1, 128, BF16, "nhd"),
+    ([0, 5, 0, 0, 64, 65, 0], 3, 2, 2, 2, 64, F32, "nhd"),
+    ([3, 130, 1, 257, 0], 5, 1, 4, 2, 128, F32, "hnd"),
+    ([127, 128, 129, 1, 0, 2], 9, 7, 4, 2, 128, BF16, "nhd"),
+    ([255, 256, 257], 1, 0, 3, 3, 128, BF16, "hnd"),
+    ([600, 33, 385], 0, 0, 8, 1, 128, BF16, "nhd"),
+    ([600, 33, 385], 100, 3, 6, 2, 64, BF16, "nhd"),
+    ([1023], 0, 0, 2, 2, 64, BF16, "hnd"),
+    ([64] * 40, 0, 0, 2, 1, 64, BF16, "nhd"),
+    ([2049, 700], 0, 5, 2, 2, 128, BF16, "hnd"),
+    ([1] * 130, 2, 0, 5, 5, 128, BF16, "nhd"),
+]
+IDS = ["x".join(map(str, c[0][:6])) + "-" + "-".join(map(str, c[1:])) for c in CASES]
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward_against_the_definition(case):
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    lens, pad, lead, Hq, Hkv, d, dtype, order = case
+    cu, T, Q, K, V, _ = _batch(lens, pad, Hq, Hkv, d, dtype, order, 11, lead)
+    _, _, O, lse = _forward(P, cu, T, Q, K, V)
+    a, b = cu[0], cu[-1]
+    wo, wl = ref.packed(Q, K, V, cu)
+    assert (O[:, :a] == 7).all() and (O[:, b:] == 7).all() and (lse[:, :a] == 7).all() and (lse[:, b:] == 7).all()
+    if a == b:
+        return
+    vmax = float(V[:, a:b].abs().max())
+    eo = (O[:, a:b].double() - wo[:, a:b]).abs()
+    el = (lse[:, a:b].double() - wl[:, a:b]).abs()
+    if dtype == F32:
+        assert float(eo.max()) <= 2e-5 * vmax and float(el.max()) <= 2e-5
+    else:
+        assert (eo <= 2.0 ** -8 * wo[:, a:b].abs() + 2.0 ** -7 * vmax).all(), float(eo.max())
+        assert float(el.max()) <= 1e-4, float(el.max())
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_backward_against_the_formula(case):
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    lens, pad, lead, Hq, Hkv, d, dtype, order = case
+    cu, T, Q, K, V, dO = _batch(lens, pad, Hq, Hkv, d, dtype, order, 12, lead)
+    s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+    dQ, dK, dV = torch.full_like(Q, 7.0), torch.full_like(K, 7.0), torch.full_like(V, 7.0)
+    delta = torch.empty((Hq, T), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    P.packed_backward(s, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV, status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    a, b = cu[0], cu[-1]
+    for x in (dQ, dK, dV):
+        assert (x[:, :a] == 7).all() and (x[:, b:] == 7).all()
+    if a == b:
+        return
+    sl = slice(a, b)
+    want = ref.packed_grad(Q[:, sl], K[:, sl], V[:, sl], dO[:, sl], [c - a for c in cu])
+    for got, w, name in zip((dQ, dK, dV), want, ("dQ", "dK", "dV")):
+        e = (got[:, sl].double() - w).abs()
+        top = max(float(w.abs().max()), 1e-3)
+        if dtype == F32:
+            assert float(e.max()) <= 1e-4 * top, (name, float(e.max()), top)
+        else:
+            assert float(e.max()) <= 2.0 ** -5 * top, (name, float(e.max()), top)
+            if float(w.norm()) > 1e-2:
+                assert float(e.norm() / w.norm()) <= 3 * 2.0 ** -8, (name, float(e.norm() / w.norm()))
+    # the same call again gives the same bits
+    again = [torch.full_like(x, 7.0) for x in (dQ, dK, dV)]
+    P.packed_backward(s, Q, K, V, plan, O, lse, dO, delta, *again)
+    for x, y in zip(again, (dQ, dK, dV)):
+        assert torch.equal(x, y)
+
+
+def test_gradient_against_differences():
+    """fp32: (L(x + h u) - L(x - h u)) / 2h along random directions, L from the forward kernel's O in double.
+
+    h = 1e-2: the forward's O carries ~1e-6 relative error, so the quotient's noise is ~1e-6 |L terms| / h,
+    and the third-order term is ~h^2: 1 % of the directional derivative's scale covers both."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    cu, T, Q, K, V, dO = _batch([70, 1, 33], 0, 4, 2, 64, F32, "hnd", 21)
+    s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+    grads = [torch.empty_like(x) for x in (Q, K, V)]
+    P.packed_backward(s, Q, K, V, plan, O, lse, dO, torch.empty((4, T), device="cuda"), *grads)
+    g = torch.Generator().manual_seed(4)
+    for i in range(3):
+        u = torch.randn(grads[i].shape, generator=g).cuda()
+        L = []
+        for sign in (1, -1):
+            x = [Q, K, V]
+            x[i] = x[i] + sign * 1e-2 * u
+            L.append(float((_forward(P, cu, T, *x)[2].double() * dO.double()).sum()))
+        num, ana = (L[0] - L[1]) / 2e-2, float((grads[i].double() * u.double()).sum())
+        assert abs(num - ana) <= 1e-2 * float(grads[i].double().norm()) * 2, (i, num, ana)
+
+
+def test_large_scores_and_long_rows():
+    """Scores up to several hundreds: the running maximum moves by far more than the type's range of exponents."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    for dtype in (F32, BF16):
+        cu, T, Q, K, V, _ = _batch([900, 37], 0, 2, 1, 128, dtype, "nhd", 31)
+        K = (K.float() * (1 + torch.arange(T, device="cuda").reshape(1, T, 1) % 97)).to(dtype)
+        _, _, O, lse = _forward(P, cu, T, Q, K, V)
+        wo, wl = ref.packed(Q, K, V, cu)
+        # fp32 scores of size 2^9 carry 2^-24 * 2^9 * a few = 1e-4, which moves a probability by as much
+        assert float((lse.double() - wl).abs().max()) <= 1e-3
+        assert float((O.double() - wo).abs().max()) <= (2e-3 if dtype == F32 else 2.0 ** -6 * float(V.abs().max()))
+
+
+def test_bad_boundaries_do_nothing_but_report():
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    cu, T, Q, K, V, _ = _batch([100, 28], 0, 2, 2, 64, BF16, "hnd", 41)
+    s = P.packed_shape(2, T, 2, 2, 64, BF16)
+    for bad in ([0, 100, 129], [-1, 100, 128], [0, 101, 100], [0, 2 ** 31 - 1, 128]):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        plan = P.packed_plan(s, torch.tensor(bad, dtype=torch.int32, device="cuda"), status=status)
+        O = torch.full_like(Q, 3.0)
+        P.packed_forward(s, Q, K, V, plan, O, status=status)
+        torch.cuda.synchronize()
+        assert int(status) == P.PYR_EBADSEQ and (O == 3).all()
+
+
+def test_packed_under_a_graph():
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    cu, T, Q, K, V, dO = _batch([300, 40, 129], 4, 4, 2, 128, BF16, "nhd", 51)
+    s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    delta = torch.empty((4, T), device="cuda")
+    grads = [torch.zeros_like(x) for x in (Q, K, V)]
+    P.packed_backward(s, Q, K, V, plan, O, lse, dO, delta, *grads)
+    O2, lse2, g2 = torch.full_like(O, 7.0), torch.full_like(lse, 7.0), [torch.zeros_like(x) for x in grads]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        P.packed_plan(s, cut, plan)
+        P.packed_forward(s, Q, K, V, plan, O2, lse2)
+        P.packed_backward(s, Q, K, V, plan, O2, lse2, dO, delta, *g2)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    for x, y in zip(grads, g2):
+        assert torch.equal(x, y)
