@@ -161,7 +161,9 @@ int packed_forward(const packed_shape* s, const pyr_view* Q, const pyr_view* K, 
   a.plan = plan;
   a.lse = lse;
   a.status = dev_status;
-  return pyr::launch_packed_fwd_simt(g, a, (cudaStream_t)stream) == cudaSuccess ? PYR_OK : PYR_ECUDA;
+  const cudaError_t e = g.dtype == PYR_F32 ? pyr::launch_packed_fwd_simt(g, a, (cudaStream_t)stream)
+                                           : pyr::launch_packed_fwd_tc(g, a, (cudaStream_t)stream);
+  return e == cudaSuccess ? PYR_OK : PYR_ECUDA;
 }
 
 int packed_backward(const packed_shape* s, const pyr_view* Q, const pyr_view* K, const pyr_view* V,

@@ -67,6 +67,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Warm L2 with a tile of a 3-D tensor map (no shared memory, no completion to wait for).
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c0), "r"(c1),
@@ -218,6 +227,11 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 // inner elements x box_rows rows x 1 head and 128-byte swizzle (rows past the
 // end read as zeros).
 bool make_tmap_bf16_3d(CUtensorMap* m, const void* base, int inner, int rows, int heads, int box_rows = 64);
+
+// Host: 4-D TMA map over a [batches][heads][rows][d] bf16 tensor of any strides (elements, multiples of 8)
+// with a box of 64 elements x box_rows rows and 128-byte swizzle (rows past the end read as zeros).
+bool make_tmap_bf16_view(CUtensorMap* m, const void* base, int64_t batch_stride, int64_t head_stride,
+                         int64_t row_stride, int d, int64_t rows, int heads, int batches, int box_rows);
 
 // Host: 3-D TMA map over a [heads][rows][inner] fp32 tensor with a box of box_inner x box_rows x 1 and
 // no swizzle (rows past the end read as zeros).
