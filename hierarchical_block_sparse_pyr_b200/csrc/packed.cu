@@ -189,7 +189,8 @@ int packed_backward(const packed_shape* s, const pyr_view* Q, const pyr_view* K,
   a.status = dev_status;
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = pyr::launch_packed_delta(g, a, st);
-  if (e == cudaSuccess) e = pyr::launch_packed_bwd_simt(g, a, st);
+  if (e == cudaSuccess)
+    e = g.dtype == PYR_F32 ? pyr::launch_packed_bwd_simt(g, a, st) : pyr::launch_packed_bwd_tc(g, a, st);
   return e == cudaSuccess ? PYR_OK : PYR_ECUDA;
 }
 

@@ -23,7 +23,7 @@ constexpr int kListFwd = 0, kListQ = 1, kListK = 2;
 // a CTA come from one head (packed_fwd_tc.cu).
 __host__ __device__ inline int packed_tile_rows(const PackedGeo& g, int list) {
   if (g.dtype == PYR_F32) return 64;
-  return list != kListFwd ? 64 : g.G % 2 ? 256 : 128;
+  return list == kListFwd && g.G % 2 ? 256 : 128;
 }
 
 __host__ __device__ inline int64_t packed_list_cap(const PackedGeo& g, int list) {
@@ -57,6 +57,7 @@ cudaError_t launch_packed_plan(const PackedGeo& g, const int32_t* cu, int32_t* p
 cudaError_t launch_packed_fwd_simt(const PackedGeo& g, const PackedFwdArgs& a, cudaStream_t st);
 cudaError_t launch_packed_fwd_tc(const PackedGeo& g, const PackedFwdArgs& a, cudaStream_t st);
 cudaError_t launch_packed_bwd_simt(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st);
+cudaError_t launch_packed_bwd_tc(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st);
 // delta = rowsum(dO * O) of the rows of every sequence
 cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st);
 

@@ -1,0 +1,753 @@
+// Gradients of packed-prompt attention on the tcgen05 tensor cores: bf16 operands, fp32 accumulation; P and
+// dS are rounded to bf16 for the products that read them. Two kernels, so that every gradient is summed by
+// one CTA in a fixed order (no atomics): S and dP are computed twice, 7 products of 128 x 128 x D where a
+// single pass with atomic sums of dQ would need 5.
+//
+// dK/dV: a CTA owns 128 keys of a key/value head and walks the 128-row query tiles from its own to the
+//   sequence's end, over the heads of the group:
+//     S^T = K Q^T, dP^T = V dO^T           (rows = keys: P^T and dS^T come out as A operands in tensor memory)
+//     P^T = 2^(S^T c - lse2), dS^T = P^T (dP^T - delta)
+//     dV += P^T dO, dK += dS^T Q
+//   Tensor memory is full: S^T 128 columns, dP^T 128, dV D, dK D; P^T and dS^T overwrite their sources as
+//   bf16. While the softmax works on P^T(t), the tensor cores run dP^T(t) and dK(t - 1).
+// dQ: a CTA owns 128 queries of a head and walks the key tiles up to the diagonal:
+//     S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K
+//   with two S buffers (dS goes over S), one of dP, and dQ.
+// Both: persistent CTAs over the plan's lists (longest first, back and forth over the CTAs).
+//   warps 0-7  softmax: warpgroup w takes the columns 64 w .. 64 w + 63 of every row; its bf16 results go to
+//              columns 64 w .. 64 w + 31 of the buffer, so that the warpgroups never touch the other's half
+//   warp 8     TMA        warps 9, 10  MMA issuers        warp 11  lse, delta and tails (dK/dV only)
+// Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
+// stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
+#include "packed.cuh"
+#include "tc_util.cuh"
+
+namespace pyr {
+
+namespace {
+
+using namespace tc;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 384;
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ int64_t list_at(int r) {
+  return (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+}
+
+// zero the rows valid .. 127 of a 128-row operand tile (64-element halves of 128 rows x 128 bytes); one warp
+template <int D>
+__device__ __forceinline__ void zero_tail(unsigned char* tile, int valid) {
+  const int lane = threadIdx.x & 31;
+  for (int x = lane; x < (128 - valid) * 8; x += 32)
+#pragma unroll
+    for (int h = 0; h < D / 64; h++)
+      *reinterpret_cast<uint4*>(tile + h * 16384 + valid * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, int row, int head, uint64_t* bar) {
+  mbar_expect_tx(bar, 128 * D * 2);
+#pragma unroll
+  for (int h = 0; h < D / 64; h++) tma_load_4d(dst + h * 16384, map, h * 64, row, head, 0, bar);
+}
+
+// D[tmem] = A B^T over D elements, both operands 128-row tiles in shared memory
+template <int D>
+__device__ __forceinline__ void mma_nt(uint32_t d, uint64_t da, uint64_t db) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; kk++) {
+    const uint64_t o = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+    umma_bf16(d, da + o, db + o, idesc, kk > 0);
+  }
+}
+
+// D[tmem] (+)= A B over 128 rows of B: A bf16 in tensor memory, its columns 0 .. 63 of K at a, 64 .. 127 at
+// a + 64; B a 128-row tile in shared memory
+template <int D>
+__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t db, bool add) {
+  constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
+#pragma unroll
+  for (int kk = 0; kk < 8; kk++)
+    umma_bf16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, db + (uint64_t)((kk * 2048) >> 4), idesc, add || kk > 0);
+}
+
+// row of a [128][D] fp32 accumulator in tensor memory, times f, to memory
+template <int D>
+__device__ __forceinline__ void store_acc(uint32_t t, __nv_bfloat16* dst, float f, bool store) {
+  float o[32];
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    tmem_ld32(t + c, o);
+    tmem_wait_ld();
+    if (store) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        uint4 v;
+        v.x = pack_bf16(o[8 * k + 0] * f, o[8 * k + 1] * f);
+        v.y = pack_bf16(o[8 * k + 2] * f, o[8 * k + 3] * f);
+        v.z = pack_bf16(o[8 * k + 4] * f, o[8 * k + 5] * f);
+        v.w = pack_bf16(o[8 * k + 6] * f, o[8 * k + 7] * f);
+        reinterpret_cast<uint4*>(dst + c)[k] = v;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- dK, dV
+
+template <int D>
+struct KPlan {
+  static constexpr int TB = 128 * D * 2;
+  static constexpr int NS = 2;  // stages of the Q and of the dO ring
+  static constexpr int kK = 0, kV = TB, kQ = 2 * TB, kG = kQ + NS * TB;
+  static constexpr int kStat = kG + NS * TB;  // [NS][2][128] fp32: -lse2, delta
+  static constexpr int kBar = kStat + NS * 1024;
+  static constexpr int kNumBars = 2 + 6 * NS + 8;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 16 + 1024;
+};
+
+struct KItem {
+  int end, key0, hk, nq, steps;
+};
+
+__device__ __forceinline__ bool k_item(const PackedGeo& g, const int32_t* plan, int64_t at, KItem* it) {
+  const int64_t tile = at / g.Hkv;
+  if (tile >= plan[kListK]) return false;
+  const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListK)) + tile);
+  it->hk = (int)(at - tile * g.Hkv);
+  it->end = w.y;
+  it->key0 = w.z;
+  it->nq = (w.y - w.z + 127) / 128;
+  it->steps = it->nq * g.G;
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+                          PackedGeo g, PackedBwdArgs a) {
+  using PL = KPlan<D>;
+  constexpr int NS = PL::NS, TB = PL::TB;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_align<1024>(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PL::kBar);
+  uint64_t* bar_kv_full = bars;            // K and V of the item
+  uint64_t* bar_kv_free = bars + 1;        // both issuers have read them
+  uint64_t* bar_q_full = bars + 2;         // [NS]
+  uint64_t* bar_q_free = bar_q_full + NS;  // [NS]
+  uint64_t* bar_g_full = bar_q_free + NS;  // [NS] dO
+  uint64_t* bar_g_free = bar_g_full + NS;  // [NS]
+  uint64_t* bar_st_full = bar_g_free + NS;   // [NS] lse and delta there, tails zeroed
+  uint64_t* bar_st_free = bar_st_full + NS;  // [NS]
+  uint64_t* bar_s_full = bar_st_free + NS;
+  uint64_t* bar_p_full = bar_s_full + 1;
+  uint64_t* bar_dp_full = bar_p_full + 1;
+  uint64_t* bar_ds_full = bar_dp_full + 1;
+  uint64_t* bar_acc_full = bar_ds_full + 1;
+  uint64_t* bar_acc_free = bar_acc_full + 1;
+  uint64_t* bar_drain = bar_acc_free + 1;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_kv_full, 1);
+    mbar_init(bar_kv_free, 2);
+    for (int s = 0; s < NS; s++) {
+      mbar_init(bar_q_full + s, 1);
+      mbar_init(bar_q_free + s, 1);
+      mbar_init(bar_g_full + s, 1);
+      mbar_init(bar_g_free + s, 2);
+      mbar_init(bar_st_full + s, 1);
+      mbar_init(bar_st_free + s, 8);
+    }
+    mbar_init(bar_s_full, 1);
+    mbar_init(bar_p_full, 8);
+    mbar_init(bar_dp_full, 1);
+    mbar_init(bar_ds_full, 8);
+    mbar_init(bar_acc_full, 2);
+    mbar_init(bar_acc_free, 8);
+    mbar_init(bar_drain, 1);
+    mbar_init(bar_drain + 1, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
+  const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024), dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
+  KItem it;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int items = 0, u = 0;
+      for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+        if (items > 0) ok = mbar_wait(bar_kv_free, (items - 1) & 1, abort_flag);
+        if (!ok) break;
+        mbar_expect_tx(bar_kv_full, 2 * TB);
+        for (int h = 0; h < D / 64; h++) {
+          tma_load_4d(smem + PL::kK + h * 16384, &tmK, h * 64, it.key0, it.hk, 0, bar_kv_full);
+          tma_load_4d(smem + PL::kV + h * 16384, &tmV, h * 64, it.key0, it.hk, 0, bar_kv_full);
+        }
+        for (int i = 0; i < it.steps && ok; i++, u++) {
+          const int s = u % NS, k = u / NS, head = it.hk * g.G + i / it.nq, q0 = it.key0 + i % it.nq * 128;
+          if (k > 0) ok = mbar_wait(bar_q_free + s, (k - 1) & 1, abort_flag);
+          if (ok && k > 0) ok = mbar_wait(bar_g_free + s, (k - 1) & 1, abort_flag);
+          if (!ok) break;
+          load_tile<D>(smem + PL::kQ + s * TB, &tmQ, q0, head, bar_q_full + s);
+          load_tile<D>(smem + PL::kG + s * TB, &tmG, q0, head, bar_g_full + s);
+        }
+      }
+      volatile int no_abort = 0;
+      for (int v = max(0, u - NS); v < u; v++) {
+        mbar_wait(bar_q_full + v % NS, (v / NS) & 1, &no_abort);
+        mbar_wait(bar_g_full + v % NS, (v / NS) & 1, &no_abort);
+      }
+      if (items > 0) mbar_wait(bar_kv_full, (items - 1) & 1, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ S^T and dV
+    if (lane == 0) {
+      const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
+      const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16384, 1024);
+      bool ok = true;
+      int items = 0, u = 0;
+      for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+        ok = mbar_wait(bar_kv_full, items & 1, abort_flag);
+        for (int i = 0; i <= it.steps && ok; i++) {
+          if (i > 0) {  // dV of step i - 1
+            const int v = u - 1, s = v % NS;
+            ok = mbar_wait(bar_p_full, v & 1, abort_flag);
+            if (ok) ok = mbar_wait(bar_g_full + s, (v / NS) & 1, abort_flag);
+            if (ok && i == 1 && items > 0) ok = mbar_wait(bar_acc_free, (items - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            mma_acc<D>(tDV, tS, dG + (uint64_t)(s * (TB >> 4)), i > 1);
+            umma_commit(bar_g_free + s);
+          }
+          if (i < it.steps) {
+            const int s = u % NS;
+            const bool tail = it.key0 + i % it.nq * 128 + 128 > it.end;
+            ok = mbar_wait(bar_q_full + s, (u / NS) & 1, abort_flag);
+            if (ok && tail) ok = mbar_wait(bar_st_full + s, (u / NS) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            // over P^T of the step before: products of one thread run in the order of issue
+            mma_nt<D>(tS, dK, dQ + (uint64_t)(s * (TB >> 4)));
+            umma_commit(bar_s_full);
+            if (i == it.steps - 1) umma_commit(bar_kv_free);
+            u++;
+          }
+        }
+        if (ok) umma_commit(bar_acc_full);
+      }
+      umma_commit(bar_drain);
+      volatile int no_abort = 0;
+      mbar_wait(bar_drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ dP^T and dK
+    if (lane == 0) {
+      const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16384, 1024);
+      bool ok = true;
+      int items = 0, u = 0;
+      for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+        ok = mbar_wait(bar_kv_full, items & 1, abort_flag);
+        for (int i = 0; i <= it.steps && ok; i++) {
+          if (i > 0) {  // dK of step i - 1
+            const int v = u - 1, s = v % NS;
+            ok = mbar_wait(bar_ds_full, v & 1, abort_flag);
+            if (ok) ok = mbar_wait(bar_q_full + s, (v / NS) & 1, abort_flag);
+            if (ok && i == 1 && items > 0) ok = mbar_wait(bar_acc_free, (items - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            mma_acc<D>(tDK, tP, dQ + (uint64_t)(s * (TB >> 4)), i > 1);
+            umma_commit(bar_q_free + s);
+          }
+          if (i < it.steps) {
+            const int s = u % NS;
+            const bool tail = it.key0 + i % it.nq * 128 + 128 > it.end;
+            ok = mbar_wait(bar_g_full + s, (u / NS) & 1, abort_flag);
+            if (ok && tail) ok = mbar_wait(bar_st_full + s, (u / NS) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            mma_nt<D>(tP, dV, dG + (uint64_t)(s * (TB >> 4)));
+            umma_commit(bar_dp_full);
+            umma_commit(bar_g_free + s);
+            if (i == it.steps - 1) umma_commit(bar_kv_free);
+            u++;
+          }
+        }
+        if (ok) umma_commit(bar_acc_full);
+      }
+      umma_commit(bar_drain + 1);
+      volatile int no_abort = 0;
+      mbar_wait(bar_drain + 1, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ lse, delta, tails
+    bool ok = true;
+    int u = 0;
+    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++) {
+      for (int i = 0; i < it.steps; i++, u++) {
+        const int s = u % NS, k = u / NS, head = it.hk * g.G + i / it.nq, q0 = it.key0 + i % it.nq * 128;
+        if (k > 0) ok = warp_wait(bar_st_free + s, (k - 1) & 1, abort_flag);
+        if (!ok) break;
+        float* st = reinterpret_cast<float*>(smem + PL::kStat + s * 1024);
+        const int64_t at = (int64_t)head * g.T;
+#pragma unroll
+        for (int c = lane; c < 128; c += 32) {
+          const int q = q0 + c;
+          st[c] = q < it.end ? -kLog2e * a.lse[at + q] : -INFINITY;
+          st[128 + c] = q < it.end ? a.delta[at + q] : 0.f;
+        }
+        if (q0 + 128 > it.end) {
+          ok = warp_wait(bar_q_full + s, k & 1, abort_flag);
+          if (ok) ok = warp_wait(bar_g_full + s, k & 1, abort_flag);
+          if (!ok) break;
+          zero_tail<D>(smem + PL::kQ + s * TB, it.end - q0);
+          zero_tail<D>(smem + PL::kG + s * TB, it.end - q0);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_st_full + s);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2, wq = warp & 3;
+    const uint32_t base = ((uint32_t)(wq * 32) << 16) + wg * 64;
+    const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
+    const float2 scl = make_float2(sl2, sl2);
+    const int rr = wq * 32 + lane;
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+      const bool live = it.key0 + wq * 32 < it.end;
+      for (int i = 0; i < it.steps; i++, u++) {
+        const int st_i = u % NS;
+        const float4* st = reinterpret_cast<const float4*>(smem + PL::kStat + st_i * 1024) + wg * 16;
+        const bool diag = i % it.nq == 0;
+        ok = warp_wait(bar_s_full, u & 1, abort_flag);
+        if (ok) ok = warp_wait(bar_st_full + st_i, (u / NS) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        float p[64];
+        if (live) {
+          tmem_ld32(tS + base, p);
+          tmem_ld32(tS + base + 32, p + 32);
+          tmem_wait_ld();
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 16; c++) {
+            const float4 nl = st[c];
+            const float2 x = __ffma2_rn(make_float2(p[4 * c], p[4 * c + 1]), scl, make_float2(nl.x, nl.y));
+            const float2 y = __ffma2_rn(make_float2(p[4 * c + 2], p[4 * c + 3]), scl, make_float2(nl.z, nl.w));
+            p[4 * c] = ex2(x.x), p[4 * c + 1] = ex2(x.y), p[4 * c + 2] = ex2(y.x), p[4 * c + 3] = ex2(y.y);
+          }
+          if (diag) {
+#pragma unroll
+            for (int c = 0; c < 64; c++) p[c] = wg * 64 + c >= rr ? p[c] : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c++) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+          tmem_st32u(tS + base, pk);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p_full);
+        ok = warp_wait(bar_dp_full, u & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            float d[32];
+            tmem_ld32(tP + base + half * 32, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; c++) {
+              const float4 dl = st[32 + half * 8 + c];
+              const float* q = p + half * 32 + 4 * c;
+              pk[half * 16 + 2 * c] = pack_bf16(q[0] * (d[4 * c] - dl.x), q[1] * (d[4 * c + 1] - dl.y));
+              pk[half * 16 + 2 * c + 1] = pack_bf16(q[2] * (d[4 * c + 2] - dl.z), q[3] * (d[4 * c + 3] - dl.w));
+            }
+          }
+          tmem_st32u(tP + base, pk);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_ds_full);
+          mbar_arrive(bar_st_free + st_i);
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue: warpgroup 0 stores dV, warpgroup 1 dK ----
+      ok = warp_wait(bar_acc_full, items & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const int key = it.key0 + rr;
+      const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+      if (live) {
+        if (wg == 0)
+          store_acc<D>(tDV + lanes, view_at<__nv_bfloat16>(a.dv, 0, it.hk, key), 1.f, key < it.end);
+        else
+          store_acc<D>(tDK + lanes, view_at<__nv_bfloat16>(a.dk, 0, it.hk, key), scale, key < it.end);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_acc_free);
+    }
+  }
+
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) report(a.status, PYR_ETIMEOUT);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// -------------------------------------------------------------------------------------------------- dQ
+
+template <int D>
+struct QPlan {
+  static constexpr int TB = 128 * D * 2;
+  static constexpr int NK = 3, NV = 2;  // K stages (a K tile lives until dQ has read it), V stages
+  static constexpr int kQ = 0, kG = TB, kK = 2 * TB, kV = kK + NK * TB;
+  static constexpr int kBar = kV + NV * TB;
+  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 2 + 1 + 1 + 1 + 1 + 2;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kBytes = kMisc + 16 + 1024;
+};
+
+struct QItem {
+  int start, end, row0, head, hk, steps;
+};
+
+__device__ __forceinline__ bool q_item(const PackedGeo& g, const int32_t* plan, int64_t at, QItem* it) {
+  const int64_t tile = at / g.Hq;
+  if (tile >= plan[kListQ]) return false;
+  const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListQ)) + tile);
+  it->head = (int)(at - tile * g.Hq);
+  it->hk = it->head / g.G;
+  it->start = w.x;
+  it->end = w.y;
+  it->row0 = w.z;
+  it->steps = (w.z - w.x) / 128 + 1;
+  return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG, PackedGeo g,
+                        PackedBwdArgs a) {
+  using PL = QPlan<D>;
+  constexpr int NK = PL::NK, NV = PL::NV, TB = PL::TB;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_align<1024>(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PL::kBar);
+  uint64_t* bar_q_full = bars;      // Q and dO of the item
+  uint64_t* bar_q_free = bars + 1;  // both issuers have read them
+  uint64_t* bar_k_full = bars + 2;
+  uint64_t* bar_k_free = bar_k_full + NK;
+  uint64_t* bar_v_full = bar_k_free + NK;
+  uint64_t* bar_v_free = bar_v_full + NV;
+  uint64_t* bar_s_full = bar_v_free + NV;   // [2]
+  uint64_t* bar_ds_full = bar_s_full + 2;   // [2]
+  uint64_t* bar_s_free = bar_ds_full + 2;   // [2] dQ has read dS
+  uint64_t* bar_dp_full = bar_s_free + 2;
+  uint64_t* bar_dp_free = bar_dp_full + 1;
+  uint64_t* bar_acc_full = bar_dp_free + 1;
+  uint64_t* bar_acc_free = bar_acc_full + 1;
+  uint64_t* bar_drain = bar_acc_free + 1;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q_full, 1);
+    mbar_init(bar_q_free, 2);
+    for (int s = 0; s < NK; s++) {
+      mbar_init(bar_k_full + s, 1);
+      mbar_init(bar_k_free + s, 1);
+    }
+    for (int s = 0; s < NV; s++) {
+      mbar_init(bar_v_full + s, 1);
+      mbar_init(bar_v_free + s, 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(bar_s_full + i, 1);
+      mbar_init(bar_ds_full + i, 8);
+      mbar_init(bar_s_free + i, 1);
+      mbar_init(bar_drain + i, 1);
+    }
+    mbar_init(bar_dp_full, 1);
+    mbar_init(bar_dp_free, 8);
+    mbar_init(bar_acc_full, 1);
+    mbar_init(bar_acc_free, 8);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tP = tmem + 256, tDQ = tmem + 384;  // S[b] at 128 b
+  const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024);
+  QItem it;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int items = 0, u = 0;
+      for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+        if (items > 0) ok = mbar_wait(bar_q_free, (items - 1) & 1, abort_flag);
+        if (!ok) break;
+        mbar_expect_tx(bar_q_full, 2 * TB);
+        for (int h = 0; h < D / 64; h++) {
+          tma_load_4d(smem + PL::kQ + h * 16384, &tmQ, h * 64, it.row0, it.head, 0, bar_q_full);
+          tma_load_4d(smem + PL::kG + h * 16384, &tmG, h * 64, it.row0, it.head, 0, bar_q_full);
+        }
+        for (int i = 0; i < it.steps && ok; i++, u++) {
+          const int sk = u % NK, kk = u / NK, sv = u % NV, kv = u / NV;
+          if (kk > 0) ok = mbar_wait(bar_k_free + sk, (kk - 1) & 1, abort_flag);
+          if (ok && kv > 0) ok = mbar_wait(bar_v_free + sv, (kv - 1) & 1, abort_flag);
+          if (!ok) break;
+          load_tile<D>(smem + PL::kK + sk * TB, &tmK, it.start + i * 128, it.hk, bar_k_full + sk);
+          load_tile<D>(smem + PL::kV + sv * TB, &tmV, it.start + i * 128, it.hk, bar_v_full + sv);
+        }
+      }
+      volatile int no_abort = 0;
+      for (int v = max(0, u - NK); v < u; v++) mbar_wait(bar_k_full + v % NK, (v / NK) & 1, &no_abort);
+      for (int v = max(0, u - NV); v < u; v++) mbar_wait(bar_v_full + v % NV, (v / NV) & 1, &no_abort);
+      if (items > 0) mbar_wait(bar_q_full, (items - 1) & 1, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ S (and the K tile's tail)
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+      ok = warp_wait(bar_q_full, items & 1, abort_flag);
+      for (int i = 0; i < it.steps && ok; i++, u++) {
+        const int s = u % NK, b = u & 1;
+        ok = warp_wait(bar_k_full + s, (u / NK) & 1, abort_flag);
+        if (ok && u >= 2) ok = warp_wait(bar_s_free + b, ((u >> 1) - 1) & 1, abort_flag);
+        if (!ok) break;
+        const int valid = it.end - (it.start + i * 128);
+        if (valid < 128) {
+          // dQ sums over the K rows; it comes after this S, which orders the zeroing before it
+          zero_tail<D>(smem + PL::kK + s * TB, valid);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          mma_nt<D>(tS + b * 128, dQ, dK + (uint64_t)(s * (TB >> 4)));
+          umma_commit(bar_s_full + b);
+          if (i == it.steps - 1) umma_commit(bar_q_free);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      umma_commit(bar_drain);
+      volatile int no_abort = 0;
+      mbar_wait(bar_drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ dP and dQ
+    if (lane == 0) {
+      const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
+      const uint64_t dKm = sdesc_sw128(smem_u32(smem + PL::kK), 16384, 1024);
+      bool ok = true;
+      int items = 0, u = 0;
+      for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+        ok = mbar_wait(bar_q_full, items & 1, abort_flag);
+        for (int i = 0; i <= it.steps && ok; i++) {
+          if (i < it.steps) {
+            const int s = u % NV;
+            ok = mbar_wait(bar_v_full + s, (u / NV) & 1, abort_flag);
+            if (ok && u > 0) ok = mbar_wait(bar_dp_free, (u - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            mma_nt<D>(tP, dG, dV + (uint64_t)(s * (TB >> 4)));
+            umma_commit(bar_dp_full);
+            umma_commit(bar_v_free + s);
+            if (i == it.steps - 1) umma_commit(bar_q_free);
+          }
+          if (i > 0) {  // dQ of step i - 1
+            const int v = i < it.steps ? u - 1 : u - 1, b = v & 1, s = v % NK;
+            ok = mbar_wait(bar_ds_full + b, (v >> 1) & 1, abort_flag);
+            if (ok && i == 1 && items > 0) ok = mbar_wait(bar_acc_free, (items - 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            mma_acc<D>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 1);
+            umma_commit(bar_k_free + s);
+            umma_commit(bar_s_free + b);
+          }
+          if (i < it.steps) u++;
+        }
+        if (ok) umma_commit(bar_acc_full);
+      }
+      umma_commit(bar_drain + 1);
+      volatile int no_abort = 0;
+      mbar_wait(bar_drain + 1, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2, wq = warp & 3;
+    const uint32_t base = ((uint32_t)(wq * 32) << 16) + wg * 64;
+    const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
+    const int rr = wq * 32 + lane;
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+      const int row = it.row0 + rr;
+      const bool live = it.row0 + wq * 32 < it.end;
+      const int64_t at = (int64_t)it.head * g.T + min(row, it.end - 1);
+      const float nl = -kLog2e * a.lse[at], del = a.delta[at];
+      const float2 scl = make_float2(sl2, sl2), off = make_float2(nl, nl);
+      for (int i = 0; i < it.steps; i++, u++) {
+        const int b = u & 1;
+        const bool diag = i == it.steps - 1;
+        ok = warp_wait(bar_s_full + b, (u >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        float p[64];
+        if (live) {
+          tmem_ld32(tS + b * 128 + base, p);
+          tmem_ld32(tS + b * 128 + base + 32, p + 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; c++) {
+            const float2 x = __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off);
+            p[2 * c] = ex2(x.x), p[2 * c + 1] = ex2(x.y);
+          }
+        }
+        ok = warp_wait(bar_dp_full, u & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            float d[32];
+            tmem_ld32(tP + base + half * 32, d);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; c++) {
+              d[c] = p[half * 32 + c] * (d[c] - del);
+              // columns behind the row hold what must not be summed, or another sequence's values
+              if (diag) d[c] = wg * 64 + half * 32 + c <= rr ? d[c] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; c++) pk[half * 16 + c] = pack_bf16(d[2 * c], d[2 * c + 1]);
+          }
+          tmem_st32u(tS + b * 128 + base, pk);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_dp_free);
+          mbar_arrive(bar_ds_full + b);
+        }
+      }
+      if (!ok) break;
+      // ---- epilogue: each warpgroup stores half of the columns ----
+      ok = warp_wait(bar_acc_full, items & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      if (live)
+        store_acc<D / 2>(tDQ + ((uint32_t)(wq * 32) << 16) + wg * (D / 2),
+                         view_at<__nv_bfloat16>(a.dq, 0, it.head, row) + wg * (D / 2), scale, row < it.end);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_acc_free);
+    }
+  }
+
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) report(a.status, PYR_ETIMEOUT);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, mg;
+  if (!make_tmap_bf16_view(&mq, a.q.data, a.q.batch, a.q.head, a.q.row, D, g.T, g.Hq, 1, 128) ||
+      !make_tmap_bf16_view(&mk, a.k.data, a.k.batch, a.k.head, a.k.row, D, g.T, g.Hkv, 1, 128) ||
+      !make_tmap_bf16_view(&mv, a.v.data, a.v.batch, a.v.head, a.v.row, D, g.T, g.Hkv, 1, 128) ||
+      !make_tmap_bf16_view(&mg, a.dout.data, a.dout.batch, a.dout.head, a.dout.row, D, g.T, g.Hq, 1, 128))
+    return cudaErrorInvalidValue;
+  auto kk = packed_dkdv_tc_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, KPlan<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  int64_t items = packed_list_cap(g, kListK) * g.Hkv;
+  kk<<<(unsigned)(items < 148 ? items : 148), kThreads, KPlan<D>::kBytes, st>>>(mq, mk, mv, mg, g, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  auto kq = packed_dq_tc_kernel<D>;
+  e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, QPlan<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  items = packed_list_cap(g, kListQ) * g.Hq;
+  kq<<<(unsigned)(items < 148 ? items : 148), kThreads, QPlan<D>::kBytes, st>>>(mq, mk, mv, mg, g, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed_bwd_tc(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
+  return g.d == 64 ? launch_d<64>(g, a, st) : launch_d<128>(g, a, st);
+}
+
+}  // namespace pyr

@@ -224,11 +224,8 @@ cudaError_t launch_bwd(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t 
 
 cudaError_t launch_packed_fwd_simt(const PackedGeo& g, const PackedFwdArgs& a, cudaStream_t st) {
   const int64_t blocks = packed_list_cap(g, kListFwd) * g.Hq;
-  if (g.dtype == PYR_F32)
-    return g.d == 64 ? launch(packed_fwd_simt_kernel<float, 64>, blocks, kThreads, fwd_smem<64>(), g, a, st)
-                     : launch(packed_fwd_simt_kernel<float, 128>, blocks, kThreads, fwd_smem<128>(), g, a, st);
-  return g.d == 64 ? launch(packed_fwd_simt_kernel<__nv_bfloat16, 64>, blocks, kThreads, fwd_smem<64>(), g, a, st)
-                   : launch(packed_fwd_simt_kernel<__nv_bfloat16, 128>, blocks, kThreads, fwd_smem<128>(), g, a, st);
+  return g.d == 64 ? launch(packed_fwd_simt_kernel<float, 64>, blocks, kThreads, fwd_smem<64>(), g, a, st)
+                   : launch(packed_fwd_simt_kernel<float, 128>, blocks, kThreads, fwd_smem<128>(), g, a, st);
 }
 
 cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
@@ -241,8 +238,7 @@ cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cuda
 }
 
 cudaError_t launch_packed_bwd_simt(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
-  if (g.dtype == PYR_F32) return g.d == 64 ? launch_bwd<float, 64>(g, a, st) : launch_bwd<float, 128>(g, a, st);
-  return g.d == 64 ? launch_bwd<__nv_bfloat16, 64>(g, a, st) : launch_bwd<__nv_bfloat16, 128>(g, a, st);
+  return g.d == 64 ? launch_bwd<float, 64>(g, a, st) : launch_bwd<float, 128>(g, a, st);
 }
 
 }  // namespace pyr
