@@ -52,6 +52,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
 // maximum of 32 values
 __device__ __forceinline__ float max32(const float* s) {
   float a[11];
@@ -149,7 +152,10 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
   unsigned char* ring = smem + PL::kRing;
 
   FItem it;
+  // a softmax thread holds a row of 128 scores; the other warpgroup needs few registers
+  // (2 * 128 * 208 + 128 * 88 = 384 * 168)
   if (warp == 8) {
+    regs_dec();
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       bool ok = true;
@@ -192,6 +198,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
+    regs_dec();
     // ------------------------------------------------------------ S = Q K^T
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
@@ -204,11 +211,12 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
           ok = mbar_wait(bar_full + s, (u / NS) & 1, abort_flag);
           if (!ok) break;
           const uint64_t dKs = dK + (uint64_t)(s * (TB >> 4));
-          for (int mt = 0; mt < 2 && ok; mt++) {
-            if (t >= it.n[mt]) continue;
+#pragma unroll
+          for (int mt = 0; mt < 2; mt++) {
+            if (!ok || t >= it.n[mt]) continue;
             if (t == 0) ok = mbar_wait(bar_q_full + mt, nq[mt]++ & 1, abort_flag);
             if (ok && ns[mt] > 0) ok = mbar_wait(bar_pv + mt, (ns[mt] - 1) & 1, abort_flag);
-            if (!ok) break;
+            if (!ok) continue;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk++)
@@ -227,6 +235,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 10) {
+    regs_dec();
     // ------------------------------------------------------------ O += P V
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
@@ -247,8 +256,9 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
           __syncwarp();
         }
         const uint64_t dVs = dV + (uint64_t)(s * (TB >> 4));
-        for (int mt = 0; mt < 2 && ok; mt++) {
-          if (t >= it.n[mt]) continue;
+#pragma unroll
+        for (int mt = 0; mt < 2; mt++) {
+          if (!ok || t >= it.n[mt]) continue;
           // O still holds the previous item's result until its epilogue has read it
           if (t == 0 && no[mt]++ > 0) ok = warp_wait(bar_o_free + mt, (no[mt] - 2) & 1, abort_flag);
           for (int half = 0; half < 2 && ok; half++) {
@@ -263,7 +273,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
             }
             __syncwarp();
           }
-          if (!ok) break;
+          if (!ok) continue;
           np[mt]++;
           if (lane == 0) umma_commit(bar_pv + mt);
         }
@@ -277,8 +287,11 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
       mbar_wait(bar_drain + 1, 0, &no_abort);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp == 11) {
+    regs_dec();
+  } else {
     // ------------------------------------------------------------ softmax
+    regs_inc();
     const int mt = warp >> 2, wq = warp & 3;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t tS_row = tS + lane_base + mt * 128;
@@ -287,11 +300,13 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     bool ok = true;
     int n = 0;  // tiles of S seen so far
     for (int r = 0; ok && fwd_item(g, a.plan, fwd_at(r), &it); r++) {
-      if (!it.n[mt]) continue;
-      const int row = it.row[mt] + wq * 32 + lane;
-      const bool live = it.row[mt] + wq * 32 < it.end;  // some row of the warp is in the sequence
+      const int steps = mt ? it.n[1] : it.n[0], row_mt = mt ? it.row[1] : it.row[0];
+      const int head = mt ? it.head[1] : it.head[0];
+      if (!steps) continue;
+      const int row = row_mt + wq * 32 + lane;
+      const bool live = row_mt + wq * 32 < it.end;  // some row of the warp is in the sequence
       float m_ref = -INFINITY, l_sum = 0.f;
-      for (int t = 0; t < it.n[mt]; t++, n++) {
+      for (int t = 0; t < steps; t++, n++) {
         ok = warp_wait(bar_s_full + mt, n & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -304,29 +319,16 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
           continue;
         }
         const int lim = row - (it.start + t * 128) + 1;  // keys this row may see
-        const bool masked = t == it.n[mt] - 1;
-        float s[64];
-        float mx = -INFINITY;
+        const bool masked = t == steps - 1;
+        float s[128];
 #pragma unroll
-        for (int c0 = 96; c0 >= 64; c0 -= 32) {
-          float x[32];
-          tmem_ld32(tS_row + c0, x);
-          if (c0 == 64) {
-            tmem_ld32(tS_row, s);
-            tmem_ld32(tS_row + 32, s + 32);
-          }
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int c = 0; c < 32; c++) x[c] = c + c0 < lim ? x[c] : -INFINITY;
-          }
-          mx = fmaxf(mx, max32(x));
-        }
+        for (int c = 0; c < 128; c += 32) tmem_ld32(tS_row + c, s + c);
+        tmem_wait_ld();
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 64; c++) s[c] = c < lim ? s[c] : -INFINITY;
+          for (int c = 0; c < 128; c++) s[c] = c < lim ? s[c] : -INFINITY;
         }
-        mx = fmax3(mx, max32(s), max32(s + 32));
+        const float mx = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
         const float m_new = fmaxf(m_ref, mx * sl2);
         const bool need = (m_ref != -INFINITY) && (m_new > m_ref + kRescale);
         float factor = 1.f;
@@ -353,19 +355,10 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; half++) {
-          if (half) {
-            tmem_ld32(tS_row + 64, s);
-            tmem_ld32(tS_row + 96, s + 32);
-            tmem_wait_ld();
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < 64; c++) s[c] = c + 64 < lim ? s[c] : -INFINITY;
-            }
-          }
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 32; c++) {
-            const float2 x = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), scl, off);
+            const float2 x = __ffma2_rn(make_float2(s[half * 64 + 2 * c], s[half * 64 + 2 * c + 1]), scl, off);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             acc[c & 3] = __fadd2_rn(acc[c & 3], e);
             pk[c] = pack_bf16(e.x, e.y);
@@ -387,7 +380,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
       tc_fence_after();
       const bool store = row < it.end;
       const float inv = 1.f / l_sum;
-      __nv_bfloat16* dst = view_at<__nv_bfloat16>(a.o, 0, it.head[mt], row);
+      __nv_bfloat16* dst = view_at<__nv_bfloat16>(a.o, 0, head, row);
       if (live) {
         float o[32];
 #pragma unroll 1
@@ -410,7 +403,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_o_free + mt);
-      if (store && a.lse) a.lse[(int64_t)it.head[mt] * g.T + row] = (m_ref + log2f(l_sum)) * 0.6931471805599453f;
+      if (store && a.lse) a.lse[(int64_t)head * g.T + row] = (m_ref + log2f(l_sum)) * 0.6931471805599453f;
     }
   }
 
