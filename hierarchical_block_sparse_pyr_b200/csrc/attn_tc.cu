@@ -536,12 +536,13 @@ bool make_tmap_bf16_3d(CUtensorMap* m, const void* base, int inner, int rows, in
 }
 
 bool make_tmap_bf16_view(CUtensorMap* m, const void* base, int64_t batch_stride, int64_t head_stride,
-                         int64_t row_stride, int d, int64_t rows, int heads, int batches, int box_rows) {
+                         int64_t row_stride, int d, int64_t rows, int heads, int batches, int box_rows,
+                         int box_heads) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads, (cuuint64_t)batches};
   cuuint64_t strides[3] = {(cuuint64_t)row_stride * 2, (cuuint64_t)head_stride * 2, (cuuint64_t)batch_stride * 2};
-  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_heads, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

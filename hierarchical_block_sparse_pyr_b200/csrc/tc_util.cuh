@@ -229,9 +229,10 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
 bool make_tmap_bf16_3d(CUtensorMap* m, const void* base, int inner, int rows, int heads, int box_rows = 64);
 
 // Host: 4-D TMA map over a [batches][heads][rows][d] bf16 tensor of any strides (elements, multiples of 8)
-// with a box of 64 elements x box_rows rows and 128-byte swizzle (rows past the end read as zeros).
+// with a box of 64 elements x box_rows rows x box_heads heads and 128-byte swizzle (rows past the end read as zeros).
 bool make_tmap_bf16_view(CUtensorMap* m, const void* base, int64_t batch_stride, int64_t head_stride,
-                         int64_t row_stride, int d, int64_t rows, int heads, int batches, int box_rows);
+                         int64_t row_stride, int d, int64_t rows, int heads, int batches, int box_rows,
+                         int box_heads = 1);
 
 // Host: 3-D TMA map over a [heads][rows][inner] fp32 tensor with a box of box_inner x box_rows x 1 and
 // no swizzle (rows past the end read as zeros).

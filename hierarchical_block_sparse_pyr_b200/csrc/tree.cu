@@ -27,8 +27,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, T
   const int slot0 = ts.cut(c0) < first ? 1 : 0;  // the first CTA may hold another segment's end before it
   const int hk = hr / g.RG, rg = hr - hk * g.RG;
   const int rr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int r = rg * g.RR + rr;
-  if (rr >= g.RR || r >= g.rows) return;
+  int hg, t;
+  if (rr >= g.RR || !tree_row(g, rg, rr, &hg, &t)) return;
   const int n = c1 - c0 + 1;
   auto part = [&](int i) { return (int64_t)((c0 + i) * 2 + (i == 0 ? slot0 : 0)) * g.RR + rr; };
   float m = -INFINITY;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, T
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const int h = hk * g.G + r / g.T, t = r % g.T;
+  const int h = hk * g.G + hg;
   const float inv = l > 0.f ? 1.f / l : 0.f;
   T* dst = view_at<T>(a.o, b, h, t) + lane * E;
 #pragma unroll
@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, T
 
 template <typename T, int D>
 cudaError_t launch_join(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
-  const int rows = g.rows < g.RR ? g.rows : g.RR;
+  const int used = g.HM ? g.G * g.T <= 128 ? g.G * g.T : g.RR : g.G * g.T;
+  const int rows = used < g.RR ? used : g.RR;
   const dim3 grid(g.B * g.Hkv * g.RG, (rows + kJoinWarps - 1) / kJoinWarps);
   tree_join_kernel<T, D><<<grid, kJoinWarps * 32, (g.B + 1) * sizeof(int), st>>>(g, a);
   return cudaGetLastError();
@@ -79,11 +80,20 @@ int make_tree_geo(const tree_shape* s, TreeGeo* g) {
   if (s->d != 64 && s->d != 128) return PYR_EUNSUPPORTED;
   if (s->T > kTreeMaxT || s->B > 4096 || s->Hq > 65535 || s->N > (1 << 28)) return PYR_EUNSUPPORTED;
   TreeGeo t = {s->B, s->Hq, s->Hkv, s->Hq / s->Hkv, s->N, s->T, s->d, s->dtype};
-  t.rows = t.G * t.T;
-  t.RR = 64;
-  t.BK = 64;
-  t.C = 296;
-  t.RG = (t.rows + t.RR - 1) / t.RR;
+  if (t.dtype == PYR_BF16) {
+    // one CTA per SM (148): two 128-row tiles where the group's heads do not fit in one
+    t.HM = 128 / t.T;
+    t.RR = t.G > t.HM ? 256 : 128;
+    t.BK = 128;
+    t.C = 148;
+    t.RG = (t.G + t.HM * (t.RR / 128) - 1) / (t.HM * (t.RR / 128));
+  } else {
+    t.HM = 0;
+    t.RR = 64;
+    t.BK = 64;
+    t.C = 296;  // two CTAs per SM
+    t.RG = (t.G * t.T + t.RR - 1) / t.RR;
+  }
   if ((int64_t)t.B * (((int64_t)t.N + t.BK - 1) / t.BK) > 0x7fffffff ||
       (int64_t)t.B * t.Hkv * t.RG > 0x7fffffff)
     return PYR_EUNSUPPORTED;
@@ -130,7 +140,7 @@ int tree_forward(const tree_shape* s, const pyr_view* Q, const pyr_view* K, cons
   a.part_ml = a.part_o + pyr::tree_part_rows(g) * g.d;
   a.status = dev_status;
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = pyr::launch_tree_simt(g, a, st);
+  cudaError_t e = g.dtype == PYR_F32 ? pyr::launch_tree_simt(g, a, st) : pyr::launch_tree_tc(g, a, st);
   if (e == cudaSuccess) e = pyr::launch_tree_join(g, a, st);
   return e == cudaSuccess ? PYR_OK : PYR_ECUDA;
 }

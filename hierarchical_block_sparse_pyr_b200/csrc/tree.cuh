@@ -5,11 +5,12 @@
 
 namespace pyr {
 
-// Rows of a unit (sequence, key/value head): row r = g * T + t is drafted token t of the group's head g.
-// A unit's rows are cut into row groups of RR; its keys into tiles of BK.
+// Rows of a unit (sequence, key/value head): drafted token t of the group's head h. They are cut into row
+// groups of RR rows, and the keys into tiles of BK. On the CUDA cores (HM = 0) row r = h * T + t is row
+// r % RR of group r / RR; on the tensor cores a group is RR / 128 tiles that hold the T rows of HM heads each.
 struct TreeGeo {
   int B, Hq, Hkv, G, N, T, d, dtype;
-  int rows;    // G * T
+  int HM;      // heads per 128-row tile, or 0
   int RR, RG;  // rows per row group, row groups per unit
   int BK;      // keys per tile
   int C;       // CTAs the tiles are split over
@@ -27,10 +28,24 @@ struct TreeArgs {
 
 constexpr int kTreeMaxT = 64;
 
+// head of the group and token of row rr of row group rg; false: the row holds nothing
+__device__ __forceinline__ bool tree_row(const TreeGeo& g, int rg, int rr, int* h, int* t) {
+  if (g.HM) {
+    const int w = rr & 127, hl = w / g.T;
+    *h = (rg * (g.RR >> 7) + (rr >> 7)) * g.HM + hl;
+    *t = w - hl * g.T;
+    return hl < g.HM && *h < g.G;
+  }
+  const int r = rg * g.RR + rr;
+  *h = r / g.T;
+  *t = r - *h * g.T;
+  return *h < g.G;
+}
+
 // keys of sequence b, tile count; a sequence with a bad length has one tile without keys, so that some
 // CTA writes its outputs
 __device__ __forceinline__ bool tree_len(const TreeGeo& g, const TreeArgs& a, int b, int* len) {
-  *len = a.len[b];
+  *len = __ldg(a.len + b);
   return *len >= 0 && *len <= g.N - g.T;
 }
 __device__ __forceinline__ int tree_tiles(const TreeGeo& g, const TreeArgs& a, int b) {
@@ -160,6 +175,7 @@ __device__ __forceinline__ bool tree_sees(int key, int len, unsigned long long m
   return mask != 0 && (key < len || (key - len < kTreeMaxT && ((mask >> (key - len)) & 1)));
 }
 
+cudaError_t launch_tree_tc(const TreeGeo& g, const TreeArgs& a, cudaStream_t st);
 cudaError_t launch_tree_simt(const TreeGeo& g, const TreeArgs& a, cudaStream_t st);
 // joins the parts of every segment that more than one CTA worked on
 cudaError_t launch_tree_join(const TreeGeo& g, const TreeArgs& a, cudaStream_t st);

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
     if (!good) len = 0;
     __syncthreads();
     if (threadIdx.x < 32) tree_masks(g, a, b, good, &masks);
-    const int nr = min(kTile, g.rows - r0);
+    const int nr = min(kTile, g.G * g.T - r0);
     for (int i = threadIdx.x; i < kTile * (D / 8); i += kThreads) {
       const int r = i / (D / 8), c = i - r * (D / 8), ra = r0 + r;
       const T* src = r < nr ? view_at<T>(a.q, b, hk * g.G + ra / g.T, ra % g.T) + c * 8 : nullptr;
@@ -115,8 +115,7 @@ cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_tree_simt(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
-  if (g.dtype == PYR_F32) return g.d == 64 ? launch<float, 64>(g, a, st) : launch<float, 128>(g, a, st);
-  return g.d == 64 ? launch<__nv_bfloat16, 64>(g, a, st) : launch<__nv_bfloat16, 128>(g, a, st);
+  return g.d == 64 ? launch<float, 64>(g, a, st) : launch<float, 128>(g, a, st);
 }
 
 }  // namespace pyr

@@ -1,0 +1,539 @@
+// Attention of drafted trees over a cache on the tcgen05 tensor cores: bf16 operands, fp32 accumulation and
+// softmax statistics. Bound by reading the cache: a tile of 128 keys and values moves 64 KB (d = 128), about
+// 2800 cycles of one SM's share of HBM, against 1024 or 2048 cycles of products.
+//
+// A persistent CTA walks its share of the stream of tiles (tree.cuh), one CTA per SM, with two slots that
+// alternate on the tensor cores: while the softmax of one slot runs, the products of the other do.
+//   SPLIT (up to 128 rows a unit): both slots hold the same rows and take the even and the odd tiles of the
+//     segment, each with its own statistics and accumulator; they are merged at the segment's end.
+//   else (two 128-row tiles): slot s holds row tile s, every K/V tile serves both.
+//   warps 0-3, 4-7  softmax of slot 0 and 1, one thread a row     warp 8   TMA
+//   warp 9          S = Q K^T     warp 10  O += P V               warp 11  the trees' masks
+// A row tile holds the T rows of 128 / T heads, in the order of the TMA box that loads them.
+// Rows of V that no token sees (behind the drafts, absent slots) are zeroed in shared memory before P V: the
+// cache may hold anything there, and 0 * NaN is NaN. Such rows of K only reach scores that are masked.
+#include "tc_util.cuh"
+#include "tree.cuh"
+
+namespace pyr {
+
+namespace {
+
+using namespace tc;
+
+constexpr float kRescale = 8.0f;
+constexpr int kThreads = 384;
+
+template <int D, bool SPLIT>
+struct TPlan {
+  static constexpr int TB = 128 * D * 2;
+  static constexpr int MT = SPLIT ? 1 : 2;
+  static constexpr int NS = D == 64 ? 8 : SPLIT ? 5 : 4;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = MT * TB;
+  static constexpr int kMasks = kRing + NS * TB;  // [2]
+  static constexpr int kMl = kMasks + 2 * (int)sizeof(TreeMaskBuf);  // [128][2] fp32: slot 1's maximum and sum
+  static constexpr int kBar = kMl + 1024;
+  static constexpr int kNumBars = 2 + 2 * NS + 2 + 4 + 2 + 2 + 4 + 2 + 2;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kSums = kMisc + 16;
+  static constexpr int kPre = kSums + 128;
+  static constexpr int kBytes = kPre + 1024;  // + 4 (B + 1)
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
+__device__ __forceinline__ float max32(const float* s) {
+  float a[11];
+#pragma unroll
+  for (int k = 0; k < 10; k++) a[k] = fmax3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
+  a[10] = fmaxf(s[30], s[31]);
+  const float x = fmax3(a[0], a[1], a[2]), y = fmax3(a[3], a[4], a[5]), z = fmax3(a[6], a[7], a[8]);
+  return fmaxf(fmax3(x, y, z), fmaxf(a[9], a[10]));
+}
+
+// a CTA's piece of a segment
+struct Seg {
+  int b, hk, rg, len, t0, steps;
+  bool good, whole, first;
+  int64_t next;
+};
+
+__device__ __forceinline__ void seg_at(const TreeGeo& g, const TreeArgs& a, const TreeStream& ts, int64_t x, int64_t x0,
+                                       int64_t x1, Seg* s) {
+  int hr, tiles;
+  int64_t at;
+  ts.find(x, &s->b, &hr, &at, &tiles);
+  s->hk = hr / g.RG;
+  s->rg = hr - s->hk * g.RG;
+  s->t0 = (int)(x - at);
+  const int t1 = (int)(x1 - at < tiles ? x1 - at : tiles);
+  s->steps = t1 - s->t0;
+  s->whole = s->t0 == 0 && t1 == tiles;
+  s->first = x == x0;
+  s->next = at + t1;
+  s->good = tree_len(g, a, s->b, &s->len);
+  if (!s->good) s->len = 0;
+}
+
+// bit c: key u0 + c, counted from the first drafted token, is visible to a row with this (non-zero) mask
+__device__ __forceinline__ unsigned long long visible64(int u0, unsigned long long mask) {
+  if (mask == 0 || u0 >= 64) return 0ull;
+  if (u0 >= 0) return mask >> u0;
+  if (u0 <= -64) return ~0ull;
+  return (mask << -u0) | ((1ull << -u0) - 1);
+}
+
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, TreeGeo g, TreeArgs a, int q_bytes) {
+  using PL = TPlan<D, SPLIT>;
+  constexpr int NS = PL::NS, TB = PL::TB, MT = PL::MT;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_align<1024>(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PL::kBar);
+  uint64_t* bar_q_full = bars;
+  uint64_t* bar_q_free = bars + 1;
+  uint64_t* bar_full = bars + 2;          // [NS]
+  uint64_t* bar_free = bar_full + NS;     // [NS]
+  uint64_t* bar_s_full = bar_free + NS;   // [2] slot
+  uint64_t* bar_p_full = bar_s_full + 2;  // [2][2] slot, half
+  uint64_t* bar_pv = bar_p_full + 4;      // [2]
+  uint64_t* bar_o_free = bar_pv + 2;      // [2]
+  uint64_t* bar_m_full = bar_o_free + 2;  // [2] masks of a segment
+  uint64_t* bar_m_free = bar_m_full + 2;  // [2]
+  uint64_t* bar_ml_full = bar_m_free + 2;
+  uint64_t* bar_ml_free = bar_ml_full + 1;
+  uint64_t* bar_drain = bar_ml_free + 1;  // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
+  TreeMaskBuf* masks = reinterpret_cast<TreeMaskBuf*>(smem + PL::kMasks);
+  float2* ml = reinterpret_cast<float2*>(smem + PL::kMl);
+  int* pre = reinterpret_cast<int*>(smem + PL::kPre);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q_full, 1);
+    mbar_init(bar_q_free, 1);
+    for (int s = 0; s < NS; s++) {
+      mbar_init(bar_full + s, 1);
+      mbar_init(bar_free + s, 1);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(bar_s_full + i, 1);
+      mbar_init(bar_p_full + 2 * i, 4);
+      mbar_init(bar_p_full + 2 * i + 1, 4);
+      mbar_init(bar_pv + i, 1);
+      mbar_init(bar_o_free + i, 4);
+      mbar_init(bar_m_full + i, 1);
+      mbar_init(bar_m_free + i, 9);  // softmax warps and the P V warp
+      mbar_init(bar_drain + i, 1);
+    }
+    mbar_init(bar_ml_full, 4);
+    mbar_init(bar_ml_free, 4);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  tree_prefix(g, a, pre, reinterpret_cast<int*>(smem + PL::kSums));
+  const TreeStream ts(g, pre);
+  if (blockIdx.x >= ts.C) return;
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tS = tmem, tO = tmem + 256;
+  unsigned char* sQ = smem + PL::kQ;
+  unsigned char* ring = smem + PL::kRing;
+  const int64_t x0 = ts.cut(blockIdx.x), x1 = ts.cut(blockIdx.x + 1);
+  Seg sg;
+
+  if (warp == 8) {
+    regs_dec();
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      bool ok = true;
+      int u = 0, segs = 0;
+      for (int64_t x = x0; x < x1 && ok; x = sg.next) {
+        seg_at(g, a, ts, x, x0, x1, &sg);
+        auto load = [&](const CUtensorMap* map, int t) {
+          const int s = u % NS, k = u / NS;
+          if (k > 0) ok = ok && mbar_wait(bar_free + s, (k - 1) & 1, abort_flag);
+          if (!ok) return;
+          mbar_expect_tx(bar_full + s, TB);
+          for (int h = 0; h < D / 64; h++)
+            tma_load_4d(ring + s * TB + h * 16384, map, h * 64, t * 128, sg.hk, sg.b, bar_full + s);
+          u++;
+        };
+        // the first K tile may be in flight while the last S of the segment before still reads Q
+        load(&tmK, sg.t0);
+        if (ok && segs > 0) ok = mbar_wait(bar_q_free, (segs - 1) & 1, abort_flag);
+        if (!ok) break;
+        mbar_expect_tx(bar_q_full, MT * q_bytes);
+        for (int mt = 0; mt < MT; mt++)
+          for (int h = 0; h < D / 64; h++)
+            tma_load_4d(sQ + mt * TB + h * 16384, &tmQ, h * 64, 0, sg.hk * g.G + (sg.rg * MT + mt) * g.HM, sg.b,
+                        bar_q_full);
+        segs++;
+        load(&tmV, sg.t0);
+        for (int i = 1; i < sg.steps && ok; i++) {
+          load(&tmK, sg.t0 + i);
+          if (ok) load(&tmV, sg.t0 + i);
+        }
+      }
+      // drain: every copy issued must land (bounded) before the CTA may exit
+      volatile int no_abort = 0;
+      if (segs > 0) mbar_wait(bar_q_full, (segs - 1) & 1, &no_abort);
+      for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    regs_dec();
+    // ------------------------------------------------------------ S = Q K^T
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
+      bool ok = true;
+      int u = 0, segs = 0, ns[2] = {0, 0};
+      for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
+        seg_at(g, a, ts, x, x0, x1, &sg);
+        for (int i = 0; i < sg.steps && ok; i++, u += 2) {
+          const int s = u % NS;
+          ok = mbar_wait(bar_full + s, (u / NS) & 1, abort_flag);
+          if (ok && i == 0) ok = mbar_wait(bar_q_full, segs & 1, abort_flag);
+          const uint64_t dKs = dK + (uint64_t)(s * (TB >> 4));
+#pragma unroll
+          for (int sl = 0; sl < 2; sl++) {
+            if (!ok || (SPLIT && sl != (i & 1))) continue;
+            if (ns[sl] > 0) ok = mbar_wait(bar_pv + sl, (ns[sl] - 1) & 1, abort_flag);
+            if (!ok) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk++)
+              umma_bf16(tS + sl * 128,
+                        dQ + (uint64_t)(((SPLIT ? 0 : sl) * TB + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                        dKs + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), idesc, kk > 0);
+            umma_commit(bar_s_full + sl);
+            ns[sl]++;
+          }
+          if (ok) umma_commit(bar_free + s);
+        }
+        if (ok) umma_commit(bar_q_free);
+      }
+      umma_commit(bar_drain);
+      volatile int no_abort = 0;
+      mbar_wait(bar_drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    regs_dec();
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
+    const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
+    bool ok = true;
+    int u = 1, segs = 0, np[2] = {0, 0}, no[2] = {0, 0};
+    for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
+      seg_at(g, a, ts, x, x0, x1, &sg);
+      unsigned long long used = 0;
+      ok = warp_wait(bar_m_full + (segs & 1), (segs >> 1) & 1, abort_flag);
+      if (!ok) break;
+      if ((sg.t0 + sg.steps) * 128 > sg.len) used = tree_used(masks + (segs & 1));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_m_free + (segs & 1));
+      for (int i = 0; i < sg.steps && ok; i++, u += 2) {
+        const int s = u % NS;
+        ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
+        if (!ok) break;
+        const int k0 = (sg.t0 + i) * 128;
+        if (k0 + 128 > sg.len) {
+          for (int r = lane; r < 128; r += 32) {
+            const int v = k0 + r - sg.len;
+            if (v < 0 || (v < g.T && ((used >> v) & 1))) continue;
+#pragma unroll
+            for (int c = 0; c < D / 8; c++)
+              *reinterpret_cast<uint4*>(ring + s * TB + (c >> 3) * 16384 + r * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const uint64_t dVs = dV + (uint64_t)(s * (TB >> 4));
+#pragma unroll
+        for (int sl = 0; sl < 2; sl++) {
+          if (!ok || (SPLIT && sl != (i & 1))) continue;
+          const bool first = i == (SPLIT ? sl : 0);
+          // O still holds the segment before until its epilogue has read it
+          if (first && no[sl]++ > 0) ok = warp_wait(bar_o_free + sl, (no[sl] - 2) & 1, abort_flag);
+          for (int half = 0; half < 2 && ok; half++) {
+            ok = warp_wait(bar_p_full + 2 * sl + half, np[sl] & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int kk = 0; kk < 4; kk++)
+                umma_bf16_ts(tO + sl * D, tS + sl * 128 + half * 32 + kk * 8,
+                             dVs + (uint64_t)(((half * 4 + kk) * 2048) >> 4), idesc, !first || half > 0 || kk > 0);
+            }
+            __syncwarp();
+          }
+          if (!ok) continue;
+          np[sl]++;
+          if (lane == 0) umma_commit(bar_pv + sl);
+        }
+        if (ok && lane == 0) umma_commit(bar_free + s);
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      umma_commit(bar_drain + 1);
+      volatile int no_abort = 0;
+      mbar_wait(bar_drain + 1, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    regs_dec();
+    // ------------------------------------------------------------ masks
+    bool ok = true;
+    int segs = 0;
+    for (int64_t x = x0; x < x1; x = sg.next, segs++) {
+      seg_at(g, a, ts, x, x0, x1, &sg);
+      if (segs >= 2) ok = warp_wait(bar_m_free + (segs & 1), ((segs >> 1) - 1) & 1, abort_flag);
+      if (!ok) break;
+      tree_masks(g, a, sg.b, sg.good, masks + (segs & 1));
+      if (lane == 0) mbar_arrive(bar_m_full + (segs & 1));
+    }
+  } else {
+    regs_inc();
+    // ------------------------------------------------------------ softmax
+    const int sl = warp >> 2, wq = warp & 3;
+    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS_row = tS + lane_base + sl * 128;
+    const uint32_t tO_row = tO + lane_base + sl * D;
+    const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
+    const int rt = wq * 32 + lane;  // row of the tile: token tok of the tile's head hl
+    const int hl = rt / g.T, tok = rt - hl * g.T;
+    bool ok = true;
+    int n = 0, n1 = 0, segs = 0, twos = 0;  // so far: S tiles of this slot, of slot 1, segments, with two slots
+    for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
+      seg_at(g, a, ts, x, x0, x1, &sg);
+      const int hg = (sg.rg * MT + (SPLIT ? 0 : sl)) * g.HM + hl;  // head of the group
+      const bool row_ok = hl < g.HM && hg < g.G;
+      ok = warp_wait(bar_m_full + (segs & 1), (segs >> 1) & 1, abort_flag);
+      if (!ok) break;
+      const unsigned long long mask = row_ok ? masks[segs & 1].mask[tok] : 0ull;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_m_free + (segs & 1));
+      const bool live = __any_sync(0xffffffffu, mask != 0);
+      float m_ref = -INFINITY, l_sum = 0.f;
+      for (int i = SPLIT ? sl : 0; i < sg.steps; i += SPLIT ? 2 : 1, n++) {
+        ok = warp_wait(bar_s_full + sl, n & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (!live) {
+          // what S left in place of P reaches rows that are not used
+          if (lane == 0) {
+            mbar_arrive(bar_p_full + 2 * sl);
+            mbar_arrive(bar_p_full + 2 * sl + 1);
+          }
+          continue;
+        }
+        const int k0 = (sg.t0 + i) * 128;
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32(tS_row + c, s + c);
+        tmem_wait_ld();
+        if (k0 + 128 > sg.len) {
+          const unsigned long long v0 = visible64(k0 - sg.len, mask), v1 = visible64(k0 + 64 - sg.len, mask);
+#pragma unroll
+          for (int c = 0; c < 64; c++) {
+            s[c] = (v0 >> c) & 1 ? s[c] : -INFINITY;
+            s[c + 64] = (v1 >> c) & 1 ? s[c + 64] : -INFINITY;
+          }
+        }
+        const float mx = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
+        const float m_new = fmaxf(m_ref, mx * sl2);
+        const bool need = (m_ref != -INFINITY) && (m_new > m_ref + kRescale);
+        float factor = 1.f;
+        if (need) {
+          factor = ex2(m_ref - m_new);
+          l_sum *= factor;
+          m_ref = m_new;
+        } else if (m_ref == -INFINITY) {
+          m_ref = m_new;
+        }
+        if (__any_sync(0xffffffffu, need)) {
+          float o[32];
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            tmem_ld32(tO_row + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; k++) o[k] *= factor;
+            tmem_st32(tO_row + c, o);
+          }
+        }
+        const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+        const float2 scl = make_float2(sl2, sl2), off = make_float2(-m_use, -m_use);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; c++) {
+            const float2 y = __ffma2_rn(make_float2(s[half * 64 + 2 * c], s[half * 64 + 2 * c + 1]), scl, off);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            acc[c & 3] = __fadd2_rn(acc[c & 3], e);
+            pk[c] = pack_bf16(e.x, e.y);
+          }
+          tmem_st32u(tS_row + half * 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_p_full + 2 * sl + half);
+        }
+        const float2 s01 = __fadd2_rn(acc[0], acc[1]), s23 = __fadd2_rn(acc[2], acc[3]);
+        const float2 sall = __fadd2_rn(s01, s23);
+        l_sum += sall.x + sall.y;
+      }
+      if (!ok) break;
+      // ---- the segment's end ----
+      const bool seen = mask != 0;
+      if (!seen) {
+        m_ref = -INFINITY;
+        l_sum = 0.f;
+      }
+      const bool two = SPLIT && sg.steps > 1;  // slot 1 has part of the keys
+      if (SPLIT && sl == 1) {
+        if (!two) continue;
+        if (twos > 0) ok = warp_wait(bar_ml_free, (twos - 1) & 1, abort_flag);
+        if (!ok) break;
+        ml[rt] = make_float2(m_ref, l_sum);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ml_full);
+        twos++;
+        continue;
+      }
+      // the last P V of the slot (the one before it was done when the last S arrived)
+      ok = warp_wait(bar_pv + sl, (n - 1) & 1, abort_flag);
+      float w0 = 1.f, w1 = 0.f;
+      if (two) {
+        n1 += sg.steps >> 1;
+        if (ok) ok = warp_wait(bar_ml_full, twos & 1, abort_flag);
+        if (ok) ok = warp_wait(bar_pv + 1, (n1 - 1) & 1, abort_flag);
+        if (!ok) break;
+        const float2 other = ml[rt];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ml_free);
+        twos++;
+        const float m = fmaxf(m_ref, other.x), mu = m == -INFINITY ? 0.f : m;
+        w0 = ex2(m_ref - mu);
+        w1 = ex2(other.x - mu);
+        m_ref = m;
+        l_sum = l_sum * w0 + other.y * w1;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const int head = sg.hk * g.G + hg;
+      const int64_t part =
+          (int64_t)(blockIdx.x * 2 + (sg.first ? 0 : 1)) * g.RR + (SPLIT ? 0 : sl) * 128 + rt;
+      if (sg.whole) {
+        const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (live) {
+          tmem_ld32(tO_row + c, o);
+          if (two) {
+            float o1[32];
+            tmem_ld32(tO_row + D + c, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; k++) o[k] = fmaf(o1[k], w1, o[k] * w0);
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; k++) o[k] *= w0;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k++) o[k] = seen ? o[k] : 0.f;
+        if (row_ok && sg.whole) {
+          uint4* dst = reinterpret_cast<uint4*>(view_at<__nv_bfloat16>(a.o, sg.b, head, tok) + c);
+#pragma unroll
+          for (int k = 0; k < 4; k++)
+            dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                                pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+        } else if (row_ok) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c);
+#pragma unroll
+          for (int k = 0; k < 8; k++) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar_o_free + sl);
+        if (two) mbar_arrive(bar_o_free + 1);
+      }
+      if (row_ok && sg.whole) {
+        if (a.lse)
+          a.lse[((int64_t)sg.b * g.Hq + head) * g.T + tok] =
+              l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+      } else if (row_ok) {
+        *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_sum);
+      }
+    }
+  }
+
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) report(a.status, PYR_ETIMEOUT);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
+  const int heads = g.HM < g.G ? g.HM : g.G;  // of a row tile
+  CUtensorMap mq, mk, mv;
+  if (!make_tmap_bf16_view(&mq, a.q.data, a.q.batch, a.q.head, a.q.row, D, g.T, g.Hq, g.B, g.T, heads) ||
+      !make_tmap_bf16_view(&mk, a.k.data, a.k.batch, a.k.head, a.k.row, D, g.N, g.Hkv, g.B, 128) ||
+      !make_tmap_bf16_view(&mv, a.v.data, a.v.batch, a.v.head, a.v.row, D, g.N, g.Hkv, g.B, 128))
+    return cudaErrorInvalidValue;
+  auto kern = tree_tc_kernel<D, SPLIT>;
+  const int smem = TPlan<D, SPLIT>::kBytes + 4 * (g.B + 1);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<g.C, kThreads, smem, st>>>(mq, mk, mv, g, a, heads * g.T * D * 2);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
+  if (g.RR == 128) return g.d == 64 ? launch<64, true>(g, a, st) : launch<128, true>(g, a, st);
+  return g.d == 64 ? launch<64, false>(g, a, st) : launch<128, false>(g, a, st);
+}
+
+}  // namespace pyr
