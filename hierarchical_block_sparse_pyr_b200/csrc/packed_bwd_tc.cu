@@ -20,7 +20,7 @@
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"
-#include "tc_util.cuh"
+#include "tc_softmax.cuh"
 
 namespace pyr {
 
@@ -28,22 +28,8 @@ namespace {
 
 using namespace tc;
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 384;
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, abort_flag);
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ int64_t list_at(int r) {
-  return (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
+constexpr int kFma = 0;  // of 16 exponentials, on the FMA pipe
 
 // zero the rows valid .. 127 of a 128-row operand tile (64-element halves of 128 rows x 128 bytes); one warp
 template <int D>
@@ -73,14 +59,18 @@ __device__ __forceinline__ void mma_nt(uint32_t d, uint64_t da, uint64_t db) {
   }
 }
 
-// D[tmem] (+)= A B over 128 rows of B: A bf16 in tensor memory, its columns 0 .. 63 of K at a, 64 .. 127 at
-// a + 64; B a 128-row tile in shared memory
+// D[tmem] (+)= A B over 128 rows of B: A bf16 in tensor memory, its elements 0 .. 63 of a row at a, 64 .. 127
+// at a + 64; B a 128-row tile in shared memory. chunk 0 or 1: the first or second 32 rows of each half of B;
+// -1: all.
 template <int D>
-__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t db, bool add) {
+__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t db, bool add, int chunk) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
 #pragma unroll
-  for (int kk = 0; kk < 8; kk++)
-    umma_bf16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, db + (uint64_t)((kk * 2048) >> 4), idesc, add || kk > 0);
+  for (int k = 0; k < 8; k++) {
+    const int kk = chunk < 0 ? k : (k >> 1) * 4 + chunk * 2 + (k & 1);
+    if (chunk >= 0 && k >= 4) break;
+    umma_bf16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, db + (uint64_t)((kk * 2048) >> 4), idesc, add || k > 0);
+  }
 }
 
 // row of a [128][D] fp32 accumulator in tensor memory, times f, to memory
@@ -91,17 +81,7 @@ __device__ __forceinline__ void store_acc(uint32_t t, __nv_bfloat16* dst, float 
   for (int c = 0; c < D; c += 32) {
     tmem_ld32(t + c, o);
     tmem_wait_ld();
-    if (store) {
-#pragma unroll
-      for (int k = 0; k < 4; k++) {
-        uint4 v;
-        v.x = pack_bf16(o[8 * k + 0] * f, o[8 * k + 1] * f);
-        v.y = pack_bf16(o[8 * k + 2] * f, o[8 * k + 3] * f);
-        v.z = pack_bf16(o[8 * k + 4] * f, o[8 * k + 5] * f);
-        v.w = pack_bf16(o[8 * k + 6] * f, o[8 * k + 7] * f);
-        reinterpret_cast<uint4*>(dst + c)[k] = v;
-      }
-    }
+    if (store) store32_bf16(dst + c, o, f);
   }
 }
 
@@ -112,9 +92,9 @@ struct KPlan {
   static constexpr int TB = 128 * D * 2;
   static constexpr int NS = 2;  // stages of the Q and of the dO ring
   static constexpr int kK = 0, kV = TB, kQ = 2 * TB, kG = kQ + NS * TB;
-  static constexpr int kStat = kG + NS * TB;  // [NS][2][128] fp32: -lse2, delta
+  static constexpr int kStat = kG + NS * TB;  // [NS][2][128] fp32: -lse2, -delta
   static constexpr int kBar = kStat + NS * 1024;
-  static constexpr int kNumBars = 2 + 6 * NS + 8;
+  static constexpr int kNumBars = 2 + 6 * NS + 9;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16 + 1024;
 };
@@ -125,12 +105,12 @@ struct KItem {
 
 __device__ __forceinline__ bool k_item(const PackedGeo& g, const int32_t* plan, int64_t at, KItem* it) {
   const int64_t tile = at / g.Hkv;
-  if (tile >= plan[kListK]) return false;
+  if (tile >= uniform(plan[kListK])) return false;
   const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListK)) + tile);
   it->hk = (int)(at - tile * g.Hkv);
-  it->end = w.y;
-  it->key0 = w.z;
-  it->nq = (w.y - w.z + 127) / 128;
+  it->end = uniform(w.y);
+  it->key0 = uniform(w.z);
+  it->nq = (it->end - it->key0 + 127) / 128;
   it->steps = it->nq * g.G;
   return true;
 }
@@ -146,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = smem_align<1024>(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PL::kBar);
   uint64_t* bar_kv_full = bars;            // K and V of the item
-  uint64_t* bar_kv_free = bars + 1;        // both issuers have read them
+  uint64_t* bar_kv_free = bars + 1;
   uint64_t* bar_q_full = bars + 2;         // [NS]
   uint64_t* bar_q_free = bar_q_full + NS;  // [NS]
   uint64_t* bar_g_full = bar_q_free + NS;  // [NS] dO
@@ -154,35 +134,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_st_full = bar_g_free + NS;   // [NS] lse and delta there, tails zeroed
   uint64_t* bar_st_free = bar_st_full + NS;  // [NS]
   uint64_t* bar_s_full = bar_st_free + NS;
-  uint64_t* bar_p_full = bar_s_full + 1;
-  uint64_t* bar_dp_full = bar_p_full + 1;
-  uint64_t* bar_ds_full = bar_dp_full + 1;
-  uint64_t* bar_acc_full = bar_ds_full + 1;
+  uint64_t* bar_p_full = bar_s_full + 1;    // [2] chunk
+  uint64_t* bar_dp_full = bar_p_full + 2;
+  uint64_t* bar_ds_full = bar_dp_full + 1;  // [2] chunk
+  uint64_t* bar_acc_full = bar_ds_full + 2;
   uint64_t* bar_acc_free = bar_acc_full + 1;
-  uint64_t* bar_drain = bar_acc_free + 1;  // [2]
+  uint64_t* bar_drain = bar_acc_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(bar_kv_full, 1);
-    mbar_init(bar_kv_free, 2);
+    mbar_init(bar_kv_free, 1);
     for (int s = 0; s < NS; s++) {
       mbar_init(bar_q_full + s, 1);
       mbar_init(bar_q_free + s, 1);
       mbar_init(bar_g_full + s, 1);
-      mbar_init(bar_g_free + s, 2);
+      mbar_init(bar_g_free + s, 1);
       mbar_init(bar_st_full + s, 1);
       mbar_init(bar_st_free + s, 8);
     }
     mbar_init(bar_s_full, 1);
-    mbar_init(bar_p_full, 8);
     mbar_init(bar_dp_full, 1);
-    mbar_init(bar_ds_full, 8);
-    mbar_init(bar_acc_full, 2);
+    for (int c = 0; c < 2; c++) {
+      mbar_init(bar_p_full + c, 8);
+      mbar_init(bar_ds_full + c, 8);
+    }
+    mbar_init(bar_acc_full, 1);
     mbar_init(bar_acc_free, 8);
     mbar_init(bar_drain, 1);
-    mbar_init(bar_drain + 1, 1);
     fence_mbar_init();
     *abort_flag = 0;
   }
@@ -199,118 +180,120 @@ __global__ void __launch_bounds__(kThreads, 1)
   KItem it;
 
   if (warp == 8) {
+    regs_dec();
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      bool ok = true;
-      int items = 0, u = 0;
-      for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
-        if (items > 0) ok = mbar_wait(bar_kv_free, (items - 1) & 1, abort_flag);
-        if (!ok) break;
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+      if (items > 0) ok = warp_wait(bar_kv_free, (items - 1) & 1, abort_flag);
+      if (!ok) break;
+      if (elect_one()) {
         mbar_expect_tx(bar_kv_full, 2 * TB);
         for (int h = 0; h < D / 64; h++) {
           tma_load_4d(smem + PL::kK + h * 16384, &tmK, h * 64, it.key0, it.hk, 0, bar_kv_full);
           tma_load_4d(smem + PL::kV + h * 16384, &tmV, h * 64, it.key0, it.hk, 0, bar_kv_full);
         }
-        for (int i = 0; i < it.steps && ok; i++, u++) {
-          const int s = u % NS, k = u / NS, head = it.hk * g.G + i / it.nq, q0 = it.key0 + i % it.nq * 128;
-          if (k > 0) ok = mbar_wait(bar_q_free + s, (k - 1) & 1, abort_flag);
-          if (ok && k > 0) ok = mbar_wait(bar_g_free + s, (k - 1) & 1, abort_flag);
-          if (!ok) break;
+      }
+      int head = it.hk * g.G, j = 0;
+      for (int i = 0; i < it.steps; i++, u++) {
+        const int s = u % NS, k = u / NS, q0 = it.key0 + j * 128;
+        if (k > 0) ok = warp_wait(bar_q_free + s, (k - 1) & 1, abort_flag);
+        if (ok && k > 0) ok = warp_wait(bar_g_free + s, (k - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
           load_tile<D>(smem + PL::kQ + s * TB, &tmQ, q0, head, bar_q_full + s);
           load_tile<D>(smem + PL::kG + s * TB, &tmG, q0, head, bar_g_full + s);
         }
+        if (++j == it.nq) j = 0, head++;
       }
-      volatile int no_abort = 0;
-      for (int v = max(0, u - NS); v < u; v++) {
-        mbar_wait(bar_q_full + v % NS, (v / NS) & 1, &no_abort);
-        mbar_wait(bar_g_full + v % NS, (v / NS) & 1, &no_abort);
-      }
-      if (items > 0) mbar_wait(bar_kv_full, (items - 1) & 1, &no_abort);
     }
+    // drain: every copy issued must land (bounded) before the CTA may exit
+    volatile int no_abort = 0;
+    for (int v = max(0, u - NS); v < u; v++) {
+      mbar_wait(bar_q_full + v % NS, (v / NS) & 1, &no_abort);
+      mbar_wait(bar_g_full + v % NS, (v / NS) & 1, &no_abort);
+    }
+    if (items > 0) mbar_wait(bar_kv_full, (items - 1) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 9) {
-    // ------------------------------------------------------------ S^T and dV
-    if (lane == 0) {
-      const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
-      const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16384, 1024);
-      bool ok = true;
-      int items = 0, u = 0;
-      for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
-        ok = mbar_wait(bar_kv_full, items & 1, abort_flag);
-        for (int i = 0; i <= it.steps && ok; i++) {
-          if (i > 0) {  // dV of step i - 1
-            const int v = u - 1, s = v % NS;
-            ok = mbar_wait(bar_p_full, v & 1, abort_flag);
-            if (ok) ok = mbar_wait(bar_g_full + s, (v / NS) & 1, abort_flag);
-            if (ok && i == 1 && items > 0) ok = mbar_wait(bar_acc_free, (items - 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            mma_acc<D>(tDV, tS, dG + (uint64_t)(s * (TB >> 4)), i > 1);
-            umma_commit(bar_g_free + s);
-          }
-          if (i < it.steps) {
-            const int s = u % NS;
-            const bool tail = it.key0 + i % it.nq * 128 + 128 > it.end;
-            ok = mbar_wait(bar_q_full + s, (u / NS) & 1, abort_flag);
-            if (ok && tail) ok = mbar_wait(bar_st_full + s, (u / NS) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            // over P^T of the step before: products of one thread run in the order of issue
-            mma_nt<D>(tS, dK, dQ + (uint64_t)(s * (TB >> 4)));
-            umma_commit(bar_s_full);
-            if (i == it.steps - 1) umma_commit(bar_kv_free);
-            u++;
-          }
+    regs_dec();
+    // ------------------------------------------------------------ all products, in the order that keeps
+    // S(i + 1) ahead of dK(i): the softmax waits for S, and dK(i) and dP(i + 1) fill its time
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024), dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
+    const uint64_t dQm = sdesc_sw128(smem_u32(smem + PL::kQ), 16384, 1024);
+    const uint64_t dGm = sdesc_sw128(smem_u32(smem + PL::kG), 16384, 1024);
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+      int j = 0;  // query tile that the next S reads
+      auto scores = [&](int v) {
+        const int s = v % NS;
+        ok = warp_wait(bar_q_full + s, (v / NS) & 1, abort_flag);
+        if (ok && it.key0 + j * 128 + 128 > it.end) ok = warp_wait(bar_st_full + s, (v / NS) & 1, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_nt<D>(tS, dK, dQ + (uint64_t)(s * (TB >> 4)));
+          umma_commit(bar_s_full);
         }
-        if (ok) umma_commit(bar_acc_full);
+        __syncwarp();
+        if (++j == it.nq) j = 0;
+      };
+      auto dprob = [&](int v) {
+        const int s = v % NS;
+        ok = warp_wait(bar_g_full + s, (v / NS) & 1, abort_flag);  // (a tail's zeroing: waited for above)
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_nt<D>(tP, dV, dG + (uint64_t)(s * (TB >> 4)));
+          umma_commit(bar_dp_full);
+        }
+        __syncwarp();
+      };
+      ok = warp_wait(bar_kv_full, items & 1, abort_flag);
+      if (ok) scores(u);
+      if (ok) dprob(u);
+      for (int i = 0; i < it.steps && ok; i++, u++) {
+        const int s = u % NS;
+        const uint64_t at = (uint64_t)(s * (TB >> 4));
+        if (i == 0 && items > 0) ok = warp_wait(bar_acc_free, (items - 1) & 1, abort_flag);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          if (ok) ok = warp_wait(bar_p_full + c, u & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_acc<D>(tDV, tS, dGm + at, i > 0 || c > 0, c);
+            if (c == 1) umma_commit(bar_g_free + s);
+          }
+          __syncwarp();
+        }
+        // over P^T(i): products of one thread run in the order of issue
+        if (ok && i + 1 < it.steps) scores(u + 1);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          if (ok) ok = warp_wait(bar_ds_full + c, u & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_acc<D>(tDK, tP, dQm + at, i > 0 || c > 0, c);
+            if (c == 1) umma_commit(bar_q_free + s);
+          }
+          __syncwarp();
+        }
+        if (ok && i + 1 < it.steps) dprob(u + 1);
       }
-      umma_commit(bar_drain);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain, 0, &no_abort);
+      if (ok && elect_one()) {
+        umma_commit(bar_kv_free);
+        umma_commit(bar_acc_full);
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    drain(bar_drain);
   } else if (warp == 10) {
-    // ------------------------------------------------------------ dP^T and dK
-    if (lane == 0) {
-      const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
-      const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16384, 1024);
-      bool ok = true;
-      int items = 0, u = 0;
-      for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
-        ok = mbar_wait(bar_kv_full, items & 1, abort_flag);
-        for (int i = 0; i <= it.steps && ok; i++) {
-          if (i > 0) {  // dK of step i - 1
-            const int v = u - 1, s = v % NS;
-            ok = mbar_wait(bar_ds_full, v & 1, abort_flag);
-            if (ok) ok = mbar_wait(bar_q_full + s, (v / NS) & 1, abort_flag);
-            if (ok && i == 1 && items > 0) ok = mbar_wait(bar_acc_free, (items - 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            mma_acc<D>(tDK, tP, dQ + (uint64_t)(s * (TB >> 4)), i > 1);
-            umma_commit(bar_q_free + s);
-          }
-          if (i < it.steps) {
-            const int s = u % NS;
-            const bool tail = it.key0 + i % it.nq * 128 + 128 > it.end;
-            ok = mbar_wait(bar_g_full + s, (u / NS) & 1, abort_flag);
-            if (ok && tail) ok = mbar_wait(bar_st_full + s, (u / NS) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            mma_nt<D>(tP, dV, dG + (uint64_t)(s * (TB >> 4)));
-            umma_commit(bar_dp_full);
-            umma_commit(bar_g_free + s);
-            if (i == it.steps - 1) umma_commit(bar_kv_free);
-            u++;
-          }
-        }
-        if (ok) umma_commit(bar_acc_full);
-      }
-      umma_commit(bar_drain + 1);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain + 1, 0, &no_abort);
-    }
-    __syncwarp();
+    regs_dec();
   } else if (warp == 11) {
+    regs_dec();
     // ------------------------------------------------------------ lse, delta, tails
     bool ok = true;
     int u = 0;
@@ -325,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = lane; c < 128; c += 32) {
           const int q = q0 + c;
           st[c] = q < it.end ? -kLog2e * a.lse[at + q] : -INFINITY;
-          st[128 + c] = q < it.end ? a.delta[at + q] : 0.f;
+          st[128 + c] = q < it.end ? -a.delta[at + q] : 0.f;
         }
         if (q0 + 128 > it.end) {
           ok = warp_wait(bar_q_full + s, k & 1, abort_flag);
@@ -341,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
+    regs_inc();
     const int wg = warp >> 2, wq = warp & 3;
     const uint32_t base = ((uint32_t)(wq * 32) << 16) + wg * 64;
     const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
@@ -363,52 +347,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tS + base, p);
           tmem_ld32(tS + base + 32, p + 32);
           tmem_wait_ld();
-          uint32_t pk[32];
-#pragma unroll
-          for (int c = 0; c < 16; c++) {
-            const float4 nl = st[c];
-            const float2 x = __ffma2_rn(make_float2(p[4 * c], p[4 * c + 1]), scl, make_float2(nl.x, nl.y));
-            const float2 y = __ffma2_rn(make_float2(p[4 * c + 2], p[4 * c + 3]), scl, make_float2(nl.z, nl.w));
-            p[4 * c] = ex2(x.x), p[4 * c + 1] = ex2(x.y), p[4 * c + 2] = ex2(y.x), p[4 * c + 3] = ex2(y.y);
-          }
-          if (diag) {
-#pragma unroll
-            for (int c = 0; c < 64; c++) p[c] = wg * 64 + c >= rr ? p[c] : 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c++) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
-          tmem_st32u(tS + base, pk);
-          tmem_wait_st();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p_full);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          if (live) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int o = 32 * c + 2 * e;
+              const float4 nl = st[8 * c + e / 2];
+              const float2 x = exp2_mix<kFma, 3>(e, __ffma2_rn(make_float2(p[o], p[o + 1]), scl, make_float2(nl.x, nl.y)));
+              const float2 y =
+                  exp2_mix<kFma, 3>(e + 1, __ffma2_rn(make_float2(p[o + 2], p[o + 3]), scl, make_float2(nl.z, nl.w)));
+              p[o] = x.x, p[o + 1] = x.y, p[o + 2] = y.x, p[o + 3] = y.y;
+            }
+            if (diag) {
+#pragma unroll
+              for (int e = 32 * c; e < 32 * c + 32; e++) p[e] = wg * 64 + e >= rr ? p[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e++) pk[e] = pack_bf16(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
+            tmem_st16u(tS + base + 16 * c, pk);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_p_full + c);
+        }
         ok = warp_wait(bar_dp_full, u & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
+        float d[64];
         if (live) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int half = 0; half < 2; half++) {
-            float d[32];
-            tmem_ld32(tP + base + half * 32, d);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 8; c++) {
-              const float4 dl = st[32 + half * 8 + c];
-              const float* q = p + half * 32 + 4 * c;
-              pk[half * 16 + 2 * c] = pack_bf16(q[0] * (d[4 * c] - dl.x), q[1] * (d[4 * c + 1] - dl.y));
-              pk[half * 16 + 2 * c + 1] = pack_bf16(q[2] * (d[4 * c + 2] - dl.z), q[3] * (d[4 * c + 3] - dl.w));
-            }
-          }
-          tmem_st32u(tP + base, pk);
-          tmem_wait_st();
+          tmem_ld32(tP + base, d);
+          tmem_ld32(tP + base + 32, d + 32);
+          tmem_wait_ld();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar_ds_full);
-          mbar_arrive(bar_st_free + st_i);
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          if (live) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int o = 32 * c + 2 * e;
+              const float4 dl = st[32 + 8 * c + e / 2];  // -delta
+              const float2 x = __fmul2_rn(make_float2(p[o], p[o + 1]), __fadd2_rn(make_float2(d[o], d[o + 1]), make_float2(dl.x, dl.y)));
+              const float2 y = __fmul2_rn(make_float2(p[o + 2], p[o + 3]), __fadd2_rn(make_float2(d[o + 2], d[o + 3]), make_float2(dl.z, dl.w)));
+              pk[e] = pack_bf16(x.x, x.y);
+              pk[e + 1] = pack_bf16(y.x, y.y);
+            }
+            tmem_st16u(tP + base + 16 * c, pk);
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_ds_full + c);
+            if (c == 1) mbar_arrive(bar_st_free + st_i);
+          }
         }
       }
       if (!ok) break;
@@ -459,14 +455,14 @@ struct QItem {
 
 __device__ __forceinline__ bool q_item(const PackedGeo& g, const int32_t* plan, int64_t at, QItem* it) {
   const int64_t tile = at / g.Hq;
-  if (tile >= plan[kListQ]) return false;
+  if (tile >= uniform(plan[kListQ])) return false;
   const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListQ)) + tile);
   it->head = (int)(at - tile * g.Hq);
   it->hk = it->head / g.G;
-  it->start = w.x;
-  it->end = w.y;
-  it->row0 = w.z;
-  it->steps = (w.z - w.x) / 128 + 1;
+  it->start = uniform(w.x);
+  it->end = uniform(w.y);
+  it->row0 = uniform(w.z);
+  it->steps = (it->row0 - it->start) / 128 + 1;
   return true;
 }
 
@@ -496,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_drain = bar_acc_free + 1;  // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(bar_q_full, 1);
@@ -535,34 +531,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   QItem it;
 
   if (warp == 8) {
+    regs_dec();
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      bool ok = true;
-      int items = 0, u = 0;
-      for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
-        if (items > 0) ok = mbar_wait(bar_q_free, (items - 1) & 1, abort_flag);
-        if (!ok) break;
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+      if (items > 0) ok = warp_wait(bar_q_free, (items - 1) & 1, abort_flag);
+      if (!ok) break;
+      if (elect_one()) {
         mbar_expect_tx(bar_q_full, 2 * TB);
         for (int h = 0; h < D / 64; h++) {
           tma_load_4d(smem + PL::kQ + h * 16384, &tmQ, h * 64, it.row0, it.head, 0, bar_q_full);
           tma_load_4d(smem + PL::kG + h * 16384, &tmG, h * 64, it.row0, it.head, 0, bar_q_full);
         }
-        for (int i = 0; i < it.steps && ok; i++, u++) {
-          const int sk = u % NK, kk = u / NK, sv = u % NV, kv = u / NV;
-          if (kk > 0) ok = mbar_wait(bar_k_free + sk, (kk - 1) & 1, abort_flag);
-          if (ok && kv > 0) ok = mbar_wait(bar_v_free + sv, (kv - 1) & 1, abort_flag);
-          if (!ok) break;
+      }
+      for (int i = 0; i < it.steps; i++, u++) {
+        const int sk = u % NK, kk = u / NK, sv = u % NV, kv = u / NV;
+        if (kk > 0) ok = warp_wait(bar_k_free + sk, (kk - 1) & 1, abort_flag);
+        if (ok && kv > 0) ok = warp_wait(bar_v_free + sv, (kv - 1) & 1, abort_flag);
+        if (!ok) break;
+        if (elect_one()) {
           load_tile<D>(smem + PL::kK + sk * TB, &tmK, it.start + i * 128, it.hk, bar_k_full + sk);
           load_tile<D>(smem + PL::kV + sv * TB, &tmV, it.start + i * 128, it.hk, bar_v_full + sv);
         }
       }
-      volatile int no_abort = 0;
-      for (int v = max(0, u - NK); v < u; v++) mbar_wait(bar_k_full + v % NK, (v / NK) & 1, &no_abort);
-      for (int v = max(0, u - NV); v < u; v++) mbar_wait(bar_v_full + v % NV, (v / NV) & 1, &no_abort);
-      if (items > 0) mbar_wait(bar_q_full, (items - 1) & 1, &no_abort);
     }
+    volatile int no_abort = 0;
+    for (int v = max(0, u - NK); v < u; v++) mbar_wait(bar_k_full + v % NK, (v / NK) & 1, &no_abort);
+    for (int v = max(0, u - NV); v < u; v++) mbar_wait(bar_v_full + v % NV, (v / NV) & 1, &no_abort);
+    if (items > 0) mbar_wait(bar_q_full, (items - 1) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 9) {
+    regs_dec();
     // ------------------------------------------------------------ S (and the K tile's tail)
     const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
     bool ok = true;
@@ -581,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) {
-          tc_fence_after();
+        tc_fence_after();
+        if (elect_one()) {
           mma_nt<D>(tS + b * 128, dQ, dK + (uint64_t)(s * (TB >> 4)));
           umma_commit(bar_s_full + b);
           if (i == it.steps - 1) umma_commit(bar_q_free);
@@ -590,55 +590,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (lane == 0) {
-      umma_commit(bar_drain);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain, 0, &no_abort);
-    }
-    __syncwarp();
+    drain(bar_drain);
   } else if (warp == 10) {
+    regs_dec();
     // ------------------------------------------------------------ dP and dQ
-    if (lane == 0) {
-      const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
-      const uint64_t dKm = sdesc_sw128(smem_u32(smem + PL::kK), 16384, 1024);
-      bool ok = true;
-      int items = 0, u = 0;
-      for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
-        ok = mbar_wait(bar_q_full, items & 1, abort_flag);
-        for (int i = 0; i <= it.steps && ok; i++) {
-          if (i < it.steps) {
-            const int s = u % NV;
-            ok = mbar_wait(bar_v_full + s, (u / NV) & 1, abort_flag);
-            if (ok && u > 0) ok = mbar_wait(bar_dp_free, (u - 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
+    const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
+    const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
+    const uint64_t dKm = sdesc_sw128(smem_u32(smem + PL::kK), 16384, 1024);
+    bool ok = true;
+    int items = 0, u = 0;
+    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+      ok = warp_wait(bar_q_full, items & 1, abort_flag);
+      for (int i = 0; i <= it.steps && ok; i++) {
+        if (i < it.steps) {
+          const int s = u % NV;
+          ok = warp_wait(bar_v_full + s, (u / NV) & 1, abort_flag);
+          if (ok && u > 0) ok = warp_wait(bar_dp_free, (u - 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
             mma_nt<D>(tP, dG, dV + (uint64_t)(s * (TB >> 4)));
             umma_commit(bar_dp_full);
             umma_commit(bar_v_free + s);
             if (i == it.steps - 1) umma_commit(bar_q_free);
           }
-          if (i > 0) {  // dQ of step i - 1
-            const int v = i < it.steps ? u - 1 : u - 1, b = v & 1, s = v % NK;
-            ok = mbar_wait(bar_ds_full + b, (v >> 1) & 1, abort_flag);
-            if (ok && i == 1 && items > 0) ok = mbar_wait(bar_acc_free, (items - 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            mma_acc<D>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 1);
+          __syncwarp();
+        }
+        if (i > 0) {  // dQ of step i - 1
+          const int v = u - 1, b = v & 1, s = v % NK;
+          ok = warp_wait(bar_ds_full + b, (v >> 1) & 1, abort_flag);
+          if (ok && i == 1 && items > 0) ok = warp_wait(bar_acc_free, (items - 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_acc<D>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 1, -1);
             umma_commit(bar_k_free + s);
             umma_commit(bar_s_free + b);
           }
-          if (i < it.steps) u++;
+          __syncwarp();
         }
-        if (ok) umma_commit(bar_acc_full);
+        if (i < it.steps) u++;
       }
-      umma_commit(bar_drain + 1);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain + 1, 0, &no_abort);
+      if (ok && elect_one()) umma_commit(bar_acc_full);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp < 8) {
+    drain(bar_drain + 1);
+  } else if (warp == 11) {
+    regs_dec();
+  } else {
     // ------------------------------------------------------------ softmax
+    regs_inc();
     const int wg = warp >> 2, wq = warp & 3;
     const uint32_t base = ((uint32_t)(wq * 32) << 16) + wg * 64;
     const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
@@ -649,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = it.row0 + rr;
       const bool live = it.row0 + wq * 32 < it.end;
       const int64_t at = (int64_t)it.head * g.T + min(row, it.end - 1);
-      const float nl = -kLog2e * a.lse[at], del = a.delta[at];
-      const float2 scl = make_float2(sl2, sl2), off = make_float2(nl, nl);
+      const float nl = -kLog2e * a.lse[at], nd = -a.delta[at];
+      const float2 scl = make_float2(sl2, sl2), off = make_float2(nl, nl), del = make_float2(nd, nd);
       for (int i = 0; i < it.steps; i++, u++) {
         const int b = u & 1;
         const bool diag = i == it.steps - 1;
@@ -664,8 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 32; c++) {
-            const float2 x = __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off);
-            p[2 * c] = ex2(x.x), p[2 * c + 1] = ex2(x.y);
+            const float2 x = exp2_mix<kFma, 3>(c & 15, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
+            p[2 * c] = x.x, p[2 * c + 1] = x.y;
           }
         }
         ok = warp_wait(bar_dp_full, u & 1, abort_flag);
@@ -673,19 +674,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (live) {
           uint32_t pk[32];
+          float d[64];
+          tmem_ld32(tP + base, d);
+          tmem_ld32(tP + base + 32, d + 32);
+          tmem_wait_ld();
+          if (diag) {
+            // columns behind the row hold what must not be summed, or another sequence's values
 #pragma unroll
-          for (int half = 0; half < 2; half++) {
-            float d[32];
-            tmem_ld32(tP + base + half * 32, d);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 32; c++) {
-              d[c] = p[half * 32 + c] * (d[c] - del);
-              // columns behind the row hold what must not be summed, or another sequence's values
-              if (diag) d[c] = wg * 64 + half * 32 + c <= rr ? d[c] : 0.f;
+            for (int c = 0; c < 64; c++) {
+              p[c] = wg * 64 + c <= rr ? p[c] : 0.f;
+              d[c] = wg * 64 + c <= rr ? d[c] : 0.f;
             }
+          }
 #pragma unroll
-            for (int c = 0; c < 16; c++) pk[half * 16 + c] = pack_bf16(d[2 * c], d[2 * c + 1]);
+          for (int c = 0; c < 32; c++) {
+            const float2 x =
+                __fmul2_rn(make_float2(p[2 * c], p[2 * c + 1]), __fadd2_rn(make_float2(d[2 * c], d[2 * c + 1]), del));
+            pk[c] = pack_bf16(x.x, x.y);
           }
           tmem_st32u(tS + b * 128 + base, pk);
           tmem_wait_st();

@@ -19,7 +19,7 @@
 // warp zeroes them in shared memory. Rows of K there only reach scores that the causal mask drops, rows of
 // Q only outputs that are not stored.
 #include "packed.cuh"
-#include "tc_util.cuh"
+#include "tc_softmax.cuh"
 
 namespace pyr {
 
@@ -27,7 +27,7 @@ namespace {
 
 using namespace tc;
 
-constexpr float kRescale = 8.0f;  // lazy rescale threshold (log2 units)
+constexpr int kFma = 0;  // of 16 exponentials, on the FMA pipe
 
 template <int D>
 struct FPlan {
@@ -42,29 +42,6 @@ struct FPlan {
   static constexpr int kThreads = 384;
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, abort_flag);
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-
-// maximum of 32 values
-__device__ __forceinline__ float max32(const float* s) {
-  float a[11];
-#pragma unroll
-  for (int k = 0; k < 10; k++) a[k] = fmax3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
-  a[10] = fmaxf(s[30], s[31]);
-  const float x = fmax3(a[0], a[1], a[2]), y = fmax3(a[3], a[4], a[5]), z = fmax3(a[6], a[7], a[8]);
-  return fmaxf(fmax3(x, y, z), fmaxf(a[9], a[10]));
-}
-
 // one unit of work of a CTA: what the two row tiles are and how many key tiles each walks
 struct FItem {
   int start, end, row0, hk;
@@ -76,12 +53,12 @@ __device__ __forceinline__ bool fwd_item(const PackedGeo& g, const int32_t* plan
   const bool pair = g.G % 2 == 0;
   const int units = pair ? g.Hq / 2 : g.Hq;
   const int64_t tile = at / units;
-  if (tile >= plan[kListFwd]) return false;
+  if (tile >= uniform(plan[kListFwd])) return false;
   const int u = (int)(at - tile * units);
-  const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListFwd)) + tile);
-  it->start = w.x;
-  it->end = w.y;
-  it->row0 = w.z;
+  int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListFwd)) + tile);
+  w.x = it->start = uniform(w.x);
+  w.y = it->end = uniform(w.y);
+  w.z = it->row0 = uniform(w.z);
 #pragma unroll
   for (int mt = 0; mt < 2; mt++) {
     it->head[mt] = pair ? 2 * u + mt : u;
@@ -91,12 +68,6 @@ __device__ __forceinline__ bool fwd_item(const PackedGeo& g, const int32_t* plan
   it->hk = it->head[0] / g.G;
   it->steps = max(it->n[0], it->n[1]);
   return true;
-}
-
-// position in the work list of a CTA's r-th item: the list is sorted by work, so going back and forth over
-// the CTAs evens out the sums
-__device__ __forceinline__ int64_t fwd_at(int r) {
-  return (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
 
 template <int D>
@@ -119,7 +90,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
   uint64_t* bar_drain = bar_o_free + 2;      // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; i++) {
@@ -157,83 +128,84 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
   if (warp == 8) {
     regs_dec();
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      bool ok = true;
-      int u = 0;  // ring uses so far
-      int nq[2] = {0, 0};
-      for (int r = 0; ok && fwd_item(g, a.plan, fwd_at(r), &it); r++) {
-        auto load_q = [&](int mt) {
-          if (!it.n[mt]) return;
-          if (nq[mt] > 0) ok = ok && mbar_wait(bar_q_free + mt, (nq[mt] - 1) & 1, abort_flag);
-          if (!ok) return;
-          mbar_expect_tx(bar_q_full + mt, TB);
-          for (int h = 0; h < D / 64; h++)
-            tma_load_4d(sQ + mt * TB + h * 16384, &tmQ, h * 64, it.row[mt], it.head[mt], 0, bar_q_full + mt);
-          nq[mt]++;
-        };
-        auto load = [&](const CUtensorMap* map, int row) {
-          const int s = u % NS, k = u / NS;
-          if (k > 0) ok = ok && mbar_wait(bar_free + s, (k - 1) & 1, abort_flag);
-          if (!ok) return;
+    bool ok = true;
+    int u = 0;  // ring uses so far
+    int nq[2] = {0, 0};
+    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
+      auto load = [&](const CUtensorMap* map, int row) {
+        const int s = u % NS, k = u / NS;
+        if (k > 0 && ok) ok = warp_wait(bar_free + s, (k - 1) & 1, abort_flag);
+        if (!ok) return;
+        if (elect_one()) {
           mbar_expect_tx(bar_full + s, TB);
           for (int h = 0; h < D / 64; h++)
             tma_load_4d(ring + s * TB + h * 16384, map, h * 64, row, it.hk, 0, bar_full + s);
-          u++;
-        };
-        // the first K tile may be in flight while the last S of the previous item still reads Q
-        load(&tmK, it.start);
-        load_q(0);
-        load_q(1);
-        if (ok) load(&tmV, it.start);
-        for (int t = 1; t < it.steps && ok; t++) {
-          load(&tmK, it.start + t * 128);
-          if (ok) load(&tmV, it.start + t * 128);
         }
+        u++;
+      };
+      // the first K tile may be in flight while the last S of the previous item still reads Q
+      load(&tmK, it.start);
+#pragma unroll
+      for (int mt = 0; mt < 2; mt++) {
+        if (!it.n[mt]) continue;
+        if (nq[mt] > 0 && ok) ok = warp_wait(bar_q_free + mt, (nq[mt] - 1) & 1, abort_flag);
+        if (!ok) continue;
+        if (elect_one()) {
+          mbar_expect_tx(bar_q_full + mt, TB);
+          for (int h = 0; h < D / 64; h++)
+            tma_load_4d(sQ + mt * TB + h * 16384, &tmQ, h * 64, it.row[mt], it.head[mt], 0, bar_q_full + mt);
+        }
+        nq[mt]++;
       }
-      // drain: every copy issued must land (bounded) before the CTA may exit
-      volatile int no_abort = 0;
-      for (int i = 0; i < 2; i++)
-        if (nq[i] > 0) mbar_wait(bar_q_full + i, (nq[i] - 1) & 1, &no_abort);
-      for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
+      load(&tmV, it.start);
+      for (int t = 1; t < it.steps && ok; t++) {
+        load(&tmK, it.start + t * 128);
+        load(&tmV, it.start + t * 128);
+      }
     }
+    // drain: every copy issued must land (bounded) before the CTA may exit
+    volatile int no_abort = 0;
+    for (int i = 0; i < 2; i++)
+      if (nq[i] > 0) mbar_wait(bar_q_full + i, (nq[i] - 1) & 1, &no_abort);
+    for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 9) {
     regs_dec();
     // ------------------------------------------------------------ S = Q K^T
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
-      bool ok = true;
-      int u = 0, nq[2] = {0, 0}, ns[2] = {0, 0};
-      for (int r = 0; ok && fwd_item(g, a.plan, fwd_at(r), &it); r++) {
-        for (int t = 0; t < it.steps && ok; t++, u += 2) {
-          const int s = u % NS;
-          ok = mbar_wait(bar_full + s, (u / NS) & 1, abort_flag);
-          if (!ok) break;
-          const uint64_t dKs = dK + (uint64_t)(s * (TB >> 4));
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
+    bool ok = true;
+    int u = 0, nq[2] = {0, 0}, ns[2] = {0, 0};
+    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
+      for (int t = 0; t < it.steps; t++, u += 2) {
+        const int s = u % NS;
+        ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
+        if (!ok) break;
+        const uint64_t dKs = dK + (uint64_t)(s * (TB >> 4));
 #pragma unroll
-          for (int mt = 0; mt < 2; mt++) {
-            if (!ok || t >= it.n[mt]) continue;
-            if (t == 0) ok = mbar_wait(bar_q_full + mt, nq[mt]++ & 1, abort_flag);
-            if (ok && ns[mt] > 0) ok = mbar_wait(bar_pv + mt, (ns[mt] - 1) & 1, abort_flag);
-            if (!ok) continue;
-            tc_fence_after();
+        for (int mt = 0; mt < 2; mt++) {
+          if (!ok || t >= it.n[mt]) continue;
+          if (t == 0) ok = warp_wait(bar_q_full + mt, nq[mt]++ & 1, abort_flag);
+          if (ok && ns[mt] > 0) ok = warp_wait(bar_pv + mt, (ns[mt] - 1) & 1, abort_flag);
+          if (!ok) continue;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk++)
               umma_bf16(tS + mt * 128, dQ + (uint64_t)((mt * TB + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                         dKs + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), idesc, kk > 0);
             umma_commit(bar_s_full + mt);
             if (t == it.n[mt] - 1) umma_commit(bar_q_free + mt);
-            ns[mt]++;
           }
-          if (ok) umma_commit(bar_free + s);
+          __syncwarp();
+          ns[mt]++;
         }
+        if (ok && elect_one()) umma_commit(bar_free + s);
+        __syncwarp();
+        if (!ok) break;
       }
-      umma_commit(bar_drain);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain, 0, &no_abort);
     }
-    __syncwarp();
+    drain(bar_drain);
   } else if (warp == 10) {
     regs_dec();
     // ------------------------------------------------------------ O += P V
@@ -241,7 +213,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
     bool ok = true;
     int u = 1, np[2] = {0, 0}, no[2] = {0, 0};
-    for (int r = 0; ok && fwd_item(g, a.plan, fwd_at(r), &it); r++) {
+    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
       for (int t = 0; t < it.steps && ok; t++, u += 2) {
         const int s = u % NS;
         ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
@@ -265,28 +237,23 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
             ok = warp_wait(bar_p_full + 2 * mt + half, np[mt] & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 4; kk++)
                 umma_bf16_ts(tO + mt * D, tS + mt * 128 + half * 32 + kk * 8,
                              dVs + (uint64_t)(((half * 4 + kk) * 2048) >> 4), idesc, t > 0 || half > 0 || kk > 0);
+              if (half) umma_commit(bar_pv + mt);
             }
             __syncwarp();
           }
           if (!ok) continue;
           np[mt]++;
-          if (lane == 0) umma_commit(bar_pv + mt);
         }
-        if (ok && lane == 0) umma_commit(bar_free + s);
+        if (ok && elect_one()) umma_commit(bar_free + s);
         __syncwarp();
       }
     }
-    if (lane == 0) {
-      umma_commit(bar_drain + 1);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain + 1, 0, &no_abort);
-    }
-    __syncwarp();
+    drain(bar_drain + 1);
   } else if (warp == 11) {
     regs_dec();
   } else {
@@ -296,10 +263,10 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t tS_row = tS + lane_base + mt * 128;
     const uint32_t tO_row = tO + lane_base + mt * D;
-    const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
+    const float sl2 = rsqrtf((float)D) * kLog2e;
     bool ok = true;
     int n = 0;  // tiles of S seen so far
-    for (int r = 0; ok && fwd_item(g, a.plan, fwd_at(r), &it); r++) {
+    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
       const int steps = mt ? it.n[1] : it.n[0], row_mt = mt ? it.row[1] : it.row[0];
       const int head = mt ? it.head[1] : it.head[0];
       if (!steps) continue;
@@ -359,7 +326,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; c++) {
             const float2 x = __ffma2_rn(make_float2(s[half * 64 + 2 * c], s[half * 64 + 2 * c + 1]), scl, off);
-            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            const float2 e = exp2_mix<kFma, 4>(c, x);
             acc[c & 3] = __fadd2_rn(acc[c & 3], e);
             pk[c] = pack_bf16(e.x, e.y);
           }
@@ -387,23 +354,13 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
         for (int c = 0; c < D; c += 32) {
           tmem_ld32(tO_row + c, o);
           tmem_wait_ld();
-          if (store) {
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-              uint4 v;
-              v.x = pack_bf16(o[8 * k + 0] * inv, o[8 * k + 1] * inv);
-              v.y = pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-              v.z = pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-              v.w = pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
-              reinterpret_cast<uint4*>(dst + c)[k] = v;
-            }
-          }
+          if (store) store32_bf16(dst + c, o, inv);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_o_free + mt);
-      if (store && a.lse) a.lse[(int64_t)head * g.T + row] = (m_ref + log2f(l_sum)) * 0.6931471805599453f;
+      if (store && a.lse) a.lse[(int64_t)head * g.T + row] = (m_ref + log2f(l_sum)) * kLn2;
     }
   }
 

@@ -12,7 +12,7 @@
 // A row tile holds the T rows of 128 / T heads, in the order of the TMA box that loads them.
 // Rows of V that no token sees (behind the drafts, absent slots) are zeroed in shared memory before P V: the
 // cache may hold anything there, and 0 * NaN is NaN. Such rows of K only reach scores that are masked.
-#include "tc_util.cuh"
+#include "tc_softmax.cuh"
 #include "tree.cuh"
 
 namespace pyr {
@@ -21,7 +21,6 @@ namespace {
 
 using namespace tc;
 
-constexpr float kRescale = 8.0f;
 constexpr int kThreads = 384;
 
 template <int D, bool SPLIT>
@@ -41,28 +40,6 @@ struct TPlan {
   static constexpr int kBytes = kPre + 1024;  // + 4 (B + 1)
 };
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, abort_flag);
-  return __all_sync(0xffffffffu, ok);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
-
-__device__ __forceinline__ float max32(const float* s) {
-  float a[11];
-#pragma unroll
-  for (int k = 0; k < 10; k++) a[k] = fmax3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
-  a[10] = fmaxf(s[30], s[31]);
-  const float x = fmax3(a[0], a[1], a[2]), y = fmax3(a[3], a[4], a[5]), z = fmax3(a[6], a[7], a[8]);
-  return fmaxf(fmax3(x, y, z), fmaxf(a[9], a[10]));
-}
-
 // a CTA's piece of a segment
 struct Seg {
   int b, hk, rg, len, t0, steps;
@@ -75,16 +52,18 @@ __device__ __forceinline__ void seg_at(const TreeGeo& g, const TreeArgs& a, cons
   int hr, tiles;
   int64_t at;
   ts.find(x, &s->b, &hr, &at, &tiles);
+  s->b = uniform(s->b);
+  hr = uniform(hr);
   s->hk = hr / g.RG;
   s->rg = hr - s->hk * g.RG;
-  s->t0 = (int)(x - at);
+  s->t0 = uniform((int)(x - at));
   const int t1 = (int)(x1 - at < tiles ? x1 - at : tiles);
-  s->steps = t1 - s->t0;
+  s->steps = uniform(t1 - s->t0);
   s->whole = s->t0 == 0 && t1 == tiles;
   s->first = x == x0;
   s->next = at + t1;
-  s->good = tree_len(g, a, s->b, &s->len);
-  if (!s->good) s->len = 0;
+  s->good = uniform(tree_len(g, a, s->b, &s->len));
+  s->len = s->good ? uniform(s->len) : 0;
 }
 
 // bit c: key u0 + c, counted from the first drafted token, is visible to a row with this (non-zero) mask
@@ -122,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   TreeMaskBuf* masks = reinterpret_cast<TreeMaskBuf*>(smem + PL::kMasks);
   float2* ml = reinterpret_cast<float2*>(smem + PL::kMl);
   int* pre = reinterpret_cast<int*>(smem + PL::kPre);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(bar_q_full, 1);
@@ -166,80 +145,82 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     regs_dec();
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      bool ok = true;
-      int u = 0, segs = 0;
-      for (int64_t x = x0; x < x1 && ok; x = sg.next) {
-        seg_at(g, a, ts, x, x0, x1, &sg);
-        auto load = [&](const CUtensorMap* map, int t) {
-          const int s = u % NS, k = u / NS;
-          if (k > 0) ok = ok && mbar_wait(bar_free + s, (k - 1) & 1, abort_flag);
-          if (!ok) return;
+    bool ok = true;
+    int u = 0, segs = 0;
+    for (int64_t x = x0; x < x1 && ok; x = sg.next) {
+      seg_at(g, a, ts, x, x0, x1, &sg);
+      auto load = [&](const CUtensorMap* map, int t) {
+        const int s = u % NS, k = u / NS;
+        if (k > 0 && ok) ok = warp_wait(bar_free + s, (k - 1) & 1, abort_flag);
+        if (!ok) return;
+        if (elect_one()) {
           mbar_expect_tx(bar_full + s, TB);
           for (int h = 0; h < D / 64; h++)
             tma_load_4d(ring + s * TB + h * 16384, map, h * 64, t * 128, sg.hk, sg.b, bar_full + s);
-          u++;
-        };
-        // the first K tile may be in flight while the last S of the segment before still reads Q
-        load(&tmK, sg.t0);
-        if (ok && segs > 0) ok = mbar_wait(bar_q_free, (segs - 1) & 1, abort_flag);
-        if (!ok) break;
+        }
+        u++;
+      };
+      // the first K tile may be in flight while the last S of the segment before still reads Q
+      load(&tmK, sg.t0);
+      if (ok && segs > 0) ok = warp_wait(bar_q_free, (segs - 1) & 1, abort_flag);
+      if (!ok) break;
+      if (elect_one()) {
         mbar_expect_tx(bar_q_full, MT * q_bytes);
         for (int mt = 0; mt < MT; mt++)
           for (int h = 0; h < D / 64; h++)
             tma_load_4d(sQ + mt * TB + h * 16384, &tmQ, h * 64, 0, sg.hk * g.G + (sg.rg * MT + mt) * g.HM, sg.b,
                         bar_q_full);
-        segs++;
-        load(&tmV, sg.t0);
-        for (int i = 1; i < sg.steps && ok; i++) {
-          load(&tmK, sg.t0 + i);
-          if (ok) load(&tmV, sg.t0 + i);
-        }
       }
-      // drain: every copy issued must land (bounded) before the CTA may exit
-      volatile int no_abort = 0;
-      if (segs > 0) mbar_wait(bar_q_full, (segs - 1) & 1, &no_abort);
-      for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
+      segs++;
+      load(&tmV, sg.t0);
+      for (int i = 1; i < sg.steps && ok; i++) {
+        load(&tmK, sg.t0 + i);
+        load(&tmV, sg.t0 + i);
+      }
     }
+    // drain: every copy issued must land (bounded) before the CTA may exit
+    volatile int no_abort = 0;
+    if (segs > 0) mbar_wait(bar_q_full, (segs - 1) & 1, &no_abort);
+    for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 9) {
     regs_dec();
     // ------------------------------------------------------------ S = Q K^T
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
-      const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
-      bool ok = true;
-      int u = 0, segs = 0, ns[2] = {0, 0};
-      for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
-        seg_at(g, a, ts, x, x0, x1, &sg);
-        for (int i = 0; i < sg.steps && ok; i++, u += 2) {
-          const int s = u % NS;
-          ok = mbar_wait(bar_full + s, (u / NS) & 1, abort_flag);
-          if (ok && i == 0) ok = mbar_wait(bar_q_full, segs & 1, abort_flag);
-          const uint64_t dKs = dK + (uint64_t)(s * (TB >> 4));
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
+    bool ok = true;
+    int u = 0, segs = 0, ns[2] = {0, 0};
+    for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
+      seg_at(g, a, ts, x, x0, x1, &sg);
+      for (int i = 0; i < sg.steps && ok; i++, u += 2) {
+        const int s = u % NS;
+        ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
+        if (ok && i == 0) ok = warp_wait(bar_q_full, segs & 1, abort_flag);
+        const uint64_t dKs = dK + (uint64_t)(s * (TB >> 4));
 #pragma unroll
-          for (int sl = 0; sl < 2; sl++) {
-            if (!ok || (SPLIT && sl != (i & 1))) continue;
-            if (ns[sl] > 0) ok = mbar_wait(bar_pv + sl, (ns[sl] - 1) & 1, abort_flag);
-            if (!ok) continue;
-            tc_fence_after();
+        for (int sl = 0; sl < 2; sl++) {
+          if (!ok || (SPLIT && sl != (i & 1))) continue;
+          if (ns[sl] > 0) ok = warp_wait(bar_pv + sl, (ns[sl] - 1) & 1, abort_flag);
+          if (!ok) continue;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk++)
               umma_bf16(tS + sl * 128,
                         dQ + (uint64_t)(((SPLIT ? 0 : sl) * TB + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                         dKs + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), idesc, kk > 0);
             umma_commit(bar_s_full + sl);
-            ns[sl]++;
           }
-          if (ok) umma_commit(bar_free + s);
+          __syncwarp();
+          ns[sl]++;
         }
-        if (ok) umma_commit(bar_q_free);
+        if (ok && elect_one()) umma_commit(bar_free + s);
+        __syncwarp();
       }
-      umma_commit(bar_drain);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain, 0, &no_abort);
+      if (ok && elect_one()) umma_commit(bar_q_free);
+      __syncwarp();
     }
-    __syncwarp();
+    drain(bar_drain);
   } else if (warp == 10) {
     regs_dec();
     // ------------------------------------------------------------ O += P V
@@ -283,28 +264,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(bar_p_full + 2 * sl + half, np[sl] & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            if (lane == 0) {
+            if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < 4; kk++)
                 umma_bf16_ts(tO + sl * D, tS + sl * 128 + half * 32 + kk * 8,
                              dVs + (uint64_t)(((half * 4 + kk) * 2048) >> 4), idesc, !first || half > 0 || kk > 0);
+              if (half) umma_commit(bar_pv + sl);
             }
             __syncwarp();
           }
           if (!ok) continue;
           np[sl]++;
-          if (lane == 0) umma_commit(bar_pv + sl);
         }
-        if (ok && lane == 0) umma_commit(bar_free + s);
+        if (ok && elect_one()) umma_commit(bar_free + s);
         __syncwarp();
       }
     }
-    if (lane == 0) {
-      umma_commit(bar_drain + 1);
-      volatile int no_abort = 0;
-      mbar_wait(bar_drain + 1, 0, &no_abort);
-    }
-    __syncwarp();
+    drain(bar_drain + 1);
   } else if (warp == 11) {
     regs_dec();
     // ------------------------------------------------------------ masks
@@ -324,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t tS_row = tS + lane_base + sl * 128;
     const uint32_t tO_row = tO + lane_base + sl * D;
-    const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
+    const float sl2 = rsqrtf((float)D) * kLog2e;
     const int rt = wq * 32 + lane;  // row of the tile: token tok of the tile's head hl
     const int hl = rt / g.T, tok = rt - hl * g.T;
     bool ok = true;
@@ -476,11 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 32; k++) o[k] = seen ? o[k] : 0.f;
         if (row_ok && sg.whole) {
-          uint4* dst = reinterpret_cast<uint4*>(view_at<__nv_bfloat16>(a.o, sg.b, head, tok) + c);
-#pragma unroll
-          for (int k = 0; k < 4; k++)
-            dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                                pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+          store32_bf16(view_at<__nv_bfloat16>(a.o, sg.b, head, tok) + c, o, 1.f);
         } else if (row_ok) {
           float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c);
 #pragma unroll
@@ -496,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row_ok && sg.whole) {
         if (a.lse)
           a.lse[((int64_t)sg.b * g.Hq + head) * g.T + tok] =
-              l_sum > 0.f ? (m_ref + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+              l_sum > 0.f ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
       } else if (row_ok) {
         *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_sum);
       }
