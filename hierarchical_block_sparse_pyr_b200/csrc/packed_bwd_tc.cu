@@ -14,9 +14,10 @@
 //     S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K
 //   with two S buffers (dS goes over S), one of dP, and dQ.
 // Both: persistent CTAs over the plan's lists (longest first, back and forth over the CTAs).
-//   warps 0-7  softmax: warpgroup w takes the columns 64 w .. 64 w + 63 of every row; its bf16 results go to
-//              columns 64 w .. 64 w + 31 of the buffer, so that the warpgroups never touch the other's half
-//   warp 8     TMA        warps 9, 10  MMA issuers        warp 11  lse, delta and tails (dK/dV only)
+//   warps 0-15  softmax: warpgroup w takes the columns 32 w .. 32 w + 31 of every row; its bf16 results go to
+//               columns 32 w .. 32 w + 15 of the buffer, so that no warpgroup touches another's columns. Four
+//               warps a scheduler: with two, the waits and tensor-memory loads of a step were not covered
+//   warp 16     TMA      warps 17, 18  products      warp 19  lse, delta and tails (dK/dV only)
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"
@@ -28,8 +29,10 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
-constexpr int kFma = 0;  // of 16 exponentials, on the FMA pipe
+constexpr int kSoftmax = 16;                    // softmax warps
+constexpr int kThreads = (kSoftmax + 4) * 32;
+// of 16 exponentials, on the FMA pipe: dK/dV and dQ kernel
+constexpr int kFma = 6, kFmaQ = 0;
 
 // zero the rows valid .. 127 of a 128-row operand tile (64-element halves of 128 rows x 128 bytes); one warp
 template <int D>
@@ -59,26 +62,22 @@ __device__ __forceinline__ void mma_nt(uint32_t d, uint64_t da, uint64_t db) {
   }
 }
 
-// D[tmem] (+)= A B over 128 rows of B: A bf16 in tensor memory, its elements 0 .. 63 of a row at a, 64 .. 127
-// at a + 64; B a 128-row tile in shared memory. chunk 0 or 1: the first or second 32 rows of each half of B;
-// -1: all.
-template <int D>
-__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t db, bool add, int chunk) {
+// D[tmem] (+)= A B over the rows 16 K0 .. 16 (K0 + NK) - 1 of B: A bf16 in tensor memory, its elements 32 w ..
+// 32 w + 31 of a row at a + 32 w; B a 128-row tile in shared memory
+template <int D, int K0, int NK>
+__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t a, uint64_t db, bool add) {
   constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
 #pragma unroll
-  for (int k = 0; k < 8; k++) {
-    const int kk = chunk < 0 ? k : (k >> 1) * 4 + chunk * 2 + (k & 1);
-    if (chunk >= 0 && k >= 4) break;
-    umma_bf16_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, db + (uint64_t)((kk * 2048) >> 4), idesc, add || k > 0);
-  }
+  for (int kk = K0; kk < K0 + NK; kk++)
+    umma_bf16_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, db + (uint64_t)((kk * 2048) >> 4), idesc, add || kk > K0);
 }
 
-// row of a [128][D] fp32 accumulator in tensor memory, times f, to memory
-template <int D>
+// N columns of a row of an fp32 accumulator in tensor memory, times f, to memory
+template <int N>
 __device__ __forceinline__ void store_acc(uint32_t t, __nv_bfloat16* dst, float f, bool store) {
-  float o[32];
 #pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
+  for (int c = 0; c < N; c += 32) {
+    float o[32];
     tmem_ld32(t + c, o);
     tmem_wait_ld();
     if (store) store32_bf16(dst + c, o, f);
@@ -134,9 +133,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_st_full = bar_g_free + NS;   // [NS] lse and delta there, tails zeroed
   uint64_t* bar_st_free = bar_st_full + NS;  // [NS]
   uint64_t* bar_s_full = bar_st_free + NS;
-  uint64_t* bar_p_full = bar_s_full + 1;    // [2] chunk
+  uint64_t* bar_p_full = bar_s_full + 1;    // [2] half of the columns
   uint64_t* bar_dp_full = bar_p_full + 2;
-  uint64_t* bar_ds_full = bar_dp_full + 1;  // [2] chunk
+  uint64_t* bar_ds_full = bar_dp_full + 1;  // [2] half of the columns
   uint64_t* bar_acc_full = bar_ds_full + 2;
   uint64_t* bar_acc_free = bar_acc_full + 1;
   uint64_t* bar_drain = bar_acc_free + 1;
@@ -153,21 +152,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_g_full + s, 1);
       mbar_init(bar_g_free + s, 1);
       mbar_init(bar_st_full + s, 1);
-      mbar_init(bar_st_free + s, 8);
+      mbar_init(bar_st_free + s, kSoftmax);
     }
     mbar_init(bar_s_full, 1);
     mbar_init(bar_dp_full, 1);
     for (int c = 0; c < 2; c++) {
-      mbar_init(bar_p_full + c, 8);
-      mbar_init(bar_ds_full + c, 8);
+      mbar_init(bar_p_full + c, kSoftmax / 2);
+      mbar_init(bar_ds_full + c, kSoftmax / 2);
     }
     mbar_init(bar_acc_full, 1);
-    mbar_init(bar_acc_free, 8);
+    mbar_init(bar_acc_free, kSoftmax);
     mbar_init(bar_drain, 1);
     fence_mbar_init();
     *abort_flag = 0;
   }
-  if (warp == 9) {
+  if (warp == kSoftmax + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -179,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024), dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
   KItem it;
 
-  if (warp == 8) {
-    regs_dec();
+  if (warp == kSoftmax + 0) {
+    regs_dec<64>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int items = 0, u = 0;
@@ -215,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (items > 0) mbar_wait(bar_kv_full, (items - 1) & 1, &no_abort);
     __syncwarp();
-  } else if (warp == 9) {
-    regs_dec();
+  } else if (warp == kSoftmax + 1) {
+    regs_dec<64>();
     // ------------------------------------------------------------ all products, in the order that keeps
     // S(i + 1) ahead of dK(i): the softmax waits for S, and dK(i) and dP(i + 1) fill its time
     const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024), dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
@@ -263,7 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            mma_acc<D>(tDV, tS, dGm + at, i > 0 || c > 0, c);
+            if (c == 0)
+              mma_acc<D, 0, 4>(tDV, tS, dGm + at, i > 0);
+            else
+              mma_acc<D, 4, 4>(tDV, tS, dGm + at, true);
             if (c == 1) umma_commit(bar_g_free + s);
           }
           __syncwarp();
@@ -276,7 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            mma_acc<D>(tDK, tP, dQm + at, i > 0 || c > 0, c);
+            if (c == 0)
+              mma_acc<D, 0, 4>(tDK, tP, dQm + at, i > 0);
+            else
+              mma_acc<D, 4, 4>(tDK, tP, dQm + at, true);
             if (c == 1) umma_commit(bar_q_free + s);
           }
           __syncwarp();
@@ -290,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     drain(bar_drain);
-  } else if (warp == 10) {
-    regs_dec();
-  } else if (warp == 11) {
-    regs_dec();
+  } else if (warp == kSoftmax + 2) {
+    regs_dec<64>();
+  } else if (warp == kSoftmax + 3) {
+    regs_dec<64>();
     // ------------------------------------------------------------ lse, delta, tails
     bool ok = true;
     int u = 0;
@@ -324,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc();
-    const int wg = warp >> 2, wq = warp & 3;
-    const uint32_t base = ((uint32_t)(wq * 32) << 16) + wg * 64;
+    regs_inc<104>();  // 512 * 104 + 128 * 64 = 640 * 96
+    const int wg = warp >> 2, wq = warp & 3, half = wg >> 1;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16, base = lanes + wg * 32;
     const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
     const float2 scl = make_float2(sl2, sl2);
     const int rr = wq * 32 + lane;
@@ -334,92 +339,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     int items = 0, u = 0;
     for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
       const bool live = it.key0 + wq * 32 < it.end;
+      int j = 0;
       for (int i = 0; i < it.steps; i++, u++) {
         const int st_i = u % NS;
-        const float4* st = reinterpret_cast<const float4*>(smem + PL::kStat + st_i * 1024) + wg * 16;
-        const bool diag = i % it.nq == 0;
+        const float4* st = reinterpret_cast<const float4*>(smem + PL::kStat + st_i * 1024) + wg * 8;
+        const bool diag = j == 0;
+        if (++j == it.nq) j = 0;
         ok = warp_wait(bar_s_full, u & 1, abort_flag);
         if (ok) ok = warp_wait(bar_st_full + st_i, (u / NS) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        float p[64];
+        float p[32];
         if (live) {
+          uint32_t pk[16];
           tmem_ld32(tS + base, p);
-          tmem_ld32(tS + base + 32, p + 32);
           tmem_wait_ld();
-        }
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-          if (live) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int o = 32 * c + 2 * e;
-              const float4 nl = st[8 * c + e / 2];
-              const float2 x = exp2_mix<kFma, 3>(e, __ffma2_rn(make_float2(p[o], p[o + 1]), scl, make_float2(nl.x, nl.y)));
-              const float2 y =
-                  exp2_mix<kFma, 3>(e + 1, __ffma2_rn(make_float2(p[o + 2], p[o + 3]), scl, make_float2(nl.z, nl.w)));
-              p[o] = x.x, p[o + 1] = x.y, p[o + 2] = y.x, p[o + 3] = y.y;
-            }
-            if (diag) {
-#pragma unroll
-              for (int e = 32 * c; e < 32 * c + 32; e++) p[e] = wg * 64 + e >= rr ? p[e] : 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e++) pk[e] = pack_bf16(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
-            tmem_st16u(tS + base + 16 * c, pk);
-            tmem_wait_st();
+          for (int e = 0; e < 16; e += 2) {
+            const float4 nl = st[e / 2];
+            const int o = 2 * e;
+            const float2 x = exp2_mix<kFma, 3>(e, __ffma2_rn(make_float2(p[o], p[o + 1]), scl, make_float2(nl.x, nl.y)));
+            const float2 y =
+                exp2_mix<kFma, 3>(e + 1, __ffma2_rn(make_float2(p[o + 2], p[o + 3]), scl, make_float2(nl.z, nl.w)));
+            p[o] = x.x, p[o + 1] = x.y, p[o + 2] = y.x, p[o + 3] = y.y;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_p_full + c);
+          if (diag) {
+#pragma unroll
+            for (int e = 0; e < 32; e++) p[e] = wg * 32 + e >= rr ? p[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e++) pk[e] = pack_bf16(p[2 * e], p[2 * e + 1]);
+          tmem_st16u(tS + base, pk);
+          tmem_wait_st();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p_full + half);
         ok = warp_wait(bar_dp_full, u & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        float d[64];
         if (live) {
+          float d[32];
+          uint32_t pk[16];
           tmem_ld32(tP + base, d);
-          tmem_ld32(tP + base + 32, d + 32);
           tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float4 nd = st[32 + e / 2];  // -delta
+            const int o = 2 * e;
+            const float2 x = __fmul2_rn(make_float2(p[o], p[o + 1]),
+                                        __fadd2_rn(make_float2(d[o], d[o + 1]), make_float2(nd.x, nd.y)));
+            const float2 y = __fmul2_rn(make_float2(p[o + 2], p[o + 3]),
+                                        __fadd2_rn(make_float2(d[o + 2], d[o + 3]), make_float2(nd.z, nd.w)));
+            pk[e] = pack_bf16(x.x, x.y);
+            pk[e + 1] = pack_bf16(y.x, y.y);
+          }
+          tmem_st16u(tP + base, pk);
+          tmem_wait_st();
         }
-#pragma unroll
-        for (int c = 0; c < 2; c++) {
-          if (live) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int o = 32 * c + 2 * e;
-              const float4 dl = st[32 + 8 * c + e / 2];  // -delta
-              const float2 x = __fmul2_rn(make_float2(p[o], p[o + 1]), __fadd2_rn(make_float2(d[o], d[o + 1]), make_float2(dl.x, dl.y)));
-              const float2 y = __fmul2_rn(make_float2(p[o + 2], p[o + 3]), __fadd2_rn(make_float2(d[o + 2], d[o + 3]), make_float2(dl.z, dl.w)));
-              pk[e] = pack_bf16(x.x, x.y);
-              pk[e + 1] = pack_bf16(y.x, y.y);
-            }
-            tmem_st16u(tP + base + 16 * c, pk);
-            tmem_wait_st();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar_ds_full + c);
-            if (c == 1) mbar_arrive(bar_st_free + st_i);
-          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_ds_full + half);
+          mbar_arrive(bar_st_free + st_i);
         }
       }
       if (!ok) break;
-      // ---- epilogue: warpgroup 0 stores dV, warpgroup 1 dK ----
+      // ---- epilogue: two warpgroups store dV, two dK, half of the columns each ----
       ok = warp_wait(bar_acc_full, items & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      const int key = it.key0 + rr;
-      const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-      if (live) {
-        if (wg == 0)
-          store_acc<D>(tDV + lanes, view_at<__nv_bfloat16>(a.dv, 0, it.hk, key), 1.f, key < it.end);
-        else
-          store_acc<D>(tDK + lanes, view_at<__nv_bfloat16>(a.dk, 0, it.hk, key), scale, key < it.end);
-      }
+      const int key = it.key0 + rr, c0 = (wg & 1) * (D / 2);
+      if (live)
+        store_acc<D / 2>((half ? tDK : tDV) + lanes + c0,
+                         view_at<__nv_bfloat16>(half ? a.dk : a.dv, 0, it.hk, key) + c0, half ? scale : 1.f,
+                         key < it.end);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free);
@@ -430,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) report(a.status, PYR_ETIMEOUT);
-  if (warp == 9) {
+  if (warp == kSoftmax + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -507,18 +501,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(bar_s_full + i, 1);
-      mbar_init(bar_ds_full + i, 8);
+      mbar_init(bar_ds_full + i, kSoftmax);
       mbar_init(bar_s_free + i, 1);
       mbar_init(bar_drain + i, 1);
     }
     mbar_init(bar_dp_full, 1);
-    mbar_init(bar_dp_free, 8);
+    mbar_init(bar_dp_free, kSoftmax);
     mbar_init(bar_acc_full, 1);
-    mbar_init(bar_acc_free, 8);
+    mbar_init(bar_acc_free, kSoftmax);
     fence_mbar_init();
     *abort_flag = 0;
   }
-  if (warp == 9) {
+  if (warp == kSoftmax + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -530,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024);
   QItem it;
 
-  if (warp == 8) {
-    regs_dec();
+  if (warp == kSoftmax + 0) {
+    regs_dec<64>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int items = 0, u = 0;
@@ -561,8 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int v = max(0, u - NV); v < u; v++) mbar_wait(bar_v_full + v % NV, (v / NV) & 1, &no_abort);
     if (items > 0) mbar_wait(bar_q_full, (items - 1) & 1, &no_abort);
     __syncwarp();
-  } else if (warp == 9) {
-    regs_dec();
+  } else if (warp == kSoftmax + 1) {
+    regs_dec<64>();
     // ------------------------------------------------------------ S (and the K tile's tail)
     const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
     bool ok = true;
@@ -591,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     drain(bar_drain);
-  } else if (warp == 10) {
-    regs_dec();
+  } else if (warp == kSoftmax + 2) {
+    regs_dec<64>();
     // ------------------------------------------------------------ dP and dQ
     const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
     const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
@@ -623,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            mma_acc<D>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 1, -1);
+            mma_acc<D, 0, 8>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 1);
             umma_commit(bar_k_free + s);
             umma_commit(bar_s_free + b);
           }
@@ -635,13 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     drain(bar_drain + 1);
-  } else if (warp == 11) {
-    regs_dec();
+  } else if (warp == kSoftmax + 3) {
+    regs_dec<64>();
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc();
+    regs_inc<104>();  // 512 * 104 + 128 * 64 = 640 * 96
     const int wg = warp >> 2, wq = warp & 3;
-    const uint32_t base = ((uint32_t)(wq * 32) << 16) + wg * 64;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16, base = lanes + wg * 32;
     const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
     const int rr = wq * 32 + lane;
     bool ok = true;
@@ -658,14 +652,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(bar_s_full + b, (u >> 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        float p[64];
+        float p[32];
         if (live) {
           tmem_ld32(tS + b * 128 + base, p);
-          tmem_ld32(tS + b * 128 + base + 32, p + 32);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; c++) {
-            const float2 x = exp2_mix<kFma, 3>(c & 15, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
+          for (int c = 0; c < 16; c++) {
+            const float2 x = exp2_mix<kFmaQ, 3>(c, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
             p[2 * c] = x.x, p[2 * c + 1] = x.y;
           }
         }
@@ -673,26 +666,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (live) {
-          uint32_t pk[32];
-          float d[64];
+          float d[32];
+          uint32_t pk[16];
           tmem_ld32(tP + base, d);
-          tmem_ld32(tP + base + 32, d + 32);
           tmem_wait_ld();
           if (diag) {
             // columns behind the row hold what must not be summed, or another sequence's values
 #pragma unroll
-            for (int c = 0; c < 64; c++) {
-              p[c] = wg * 64 + c <= rr ? p[c] : 0.f;
-              d[c] = wg * 64 + c <= rr ? d[c] : 0.f;
+            for (int c = 0; c < 32; c++) {
+              p[c] = wg * 32 + c <= rr ? p[c] : 0.f;
+              d[c] = wg * 32 + c <= rr ? d[c] : 0.f;
             }
           }
 #pragma unroll
-          for (int c = 0; c < 32; c++) {
+          for (int c = 0; c < 16; c++) {
             const float2 x =
                 __fmul2_rn(make_float2(p[2 * c], p[2 * c + 1]), __fadd2_rn(make_float2(d[2 * c], d[2 * c + 1]), del));
             pk[c] = pack_bf16(x.x, x.y);
           }
-          tmem_st32u(tS + b * 128 + base, pk);
+          tmem_st16u(tS + b * 128 + base, pk);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -703,13 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- epilogue: each warpgroup stores half of the columns ----
+      // ---- epilogue: 32 columns a warpgroup ----
       ok = warp_wait(bar_acc_full, items & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      if (live)
-        store_acc<D / 2>(tDQ + ((uint32_t)(wq * 32) << 16) + wg * (D / 2),
-                         view_at<__nv_bfloat16>(a.dq, 0, it.head, row) + wg * (D / 2), scale, row < it.end);
+      if (live && wg * 32 < D)
+        store_acc<32>(tDQ + base, view_at<__nv_bfloat16>(a.dq, 0, it.head, row) + wg * 32, scale, row < it.end);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free);
@@ -720,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && threadIdx.x == 0) report(a.status, PYR_ETIMEOUT);
-  if (warp == 9) {
+  if (warp == kSoftmax + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

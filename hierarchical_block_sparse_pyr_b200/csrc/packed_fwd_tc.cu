@@ -27,7 +27,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kFma = 0;  // of 16 exponentials, on the FMA pipe
+constexpr int kFma = 6;  // of 16 exponentials, on the FMA pipe
 
 template <int D>
 struct FPlan {
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
   // a softmax thread holds a row of 128 scores; the other warpgroup needs few registers
   // (2 * 128 * 208 + 128 * 88 = 384 * 168)
   if (warp == 8) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int u = 0;  // ring uses so far
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 9) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ S = Q K^T
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     }
     drain(bar_drain);
   } else if (warp == 10) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ O += P V
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     }
     drain(bar_drain + 1);
   } else if (warp == 11) {
-    regs_dec();
+    regs_dec<88>();
   } else {
     // ------------------------------------------------------------ softmax
-    regs_inc();
+    regs_inc<208>();  // 2 * 128 * 208 + 128 * 88 = 384 * 168
     const int mt = warp >> 2, wq = warp & 3;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     const uint32_t tS_row = tS + lane_base + mt * 128;

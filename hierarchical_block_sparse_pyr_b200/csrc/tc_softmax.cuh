@@ -39,10 +39,16 @@ __device__ __forceinline__ void drain(uint64_t* bar) {  // every product issued 
   __syncwarp();
 }
 
-// Three warpgroups of 128 threads at 168 registers: two softmax warpgroups take 208, the third keeps 88
-// (2 * 128 * 208 + 128 * 88 = 384 * 168).
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+// Registers move from the warpgroup that loads and issues to those that hold rows of scores. The shares have
+// to add up to what the block was launched with.
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);

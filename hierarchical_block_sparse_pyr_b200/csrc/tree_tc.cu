@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seg sg;
 
   if (warp == 8) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int u = 0, segs = 0;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int v = max(0, u - NS); v < u; v++) mbar_wait(bar_full + v % NS, (v / NS) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 9) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ S = Q K^T
     constexpr uint32_t idesc = idesc_bf16_f32(128, 128, 0, 0);
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     drain(bar_drain);
   } else if (warp == 10) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ O += P V
     constexpr uint32_t idesc = idesc_bf16_f32(128, D, 0, 1);
     const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     drain(bar_drain + 1);
   } else if (warp == 11) {
-    regs_dec();
+    regs_dec<88>();
     // ------------------------------------------------------------ masks
     bool ok = true;
     int segs = 0;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar_m_full + (segs & 1));
     }
   } else {
-    regs_inc();
+    regs_inc<208>();  // 2 * 128 * 208 + 128 * 88 = 384 * 168
     // ------------------------------------------------------------ softmax
     const int sl = warp >> 2, wq = warp & 3;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
