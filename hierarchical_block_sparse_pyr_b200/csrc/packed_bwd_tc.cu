@@ -17,7 +17,8 @@
 //   warps 0-15  softmax: warpgroup w takes the columns 32 w .. 32 w + 31 of every row; its bf16 results go to
 //               columns 32 w .. 32 w + 15 of the buffer, so that no warpgroup touches another's columns. Four
 //               warps a scheduler: with two, the waits and tensor-memory loads of a step were not covered
-//   warp 16     TMA      warps 17, 18  products      warp 19  lse, delta and tails (dK/dV only)
+//   warp 16     TMA      warp 17  products (S and dQ in the dQ kernel)      warp 18  dP in the dQ kernel
+//   warp 19     lse, delta and tails (dK/dV only)
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"
@@ -438,7 +439,7 @@ struct QPlan {
   static constexpr int NK = 3, NV = 2;  // K stages (a K tile lives until dQ has read it), V stages
   static constexpr int kQ = 0, kG = TB, kK = 2 * TB, kV = kK + NK * TB;
   static constexpr int kBar = kV + NV * TB;
-  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 2 + 1 + 1 + 1 + 1 + 2;
+  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 1 + 1 + 1 + 1 + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16 + 1024;
 };
@@ -478,8 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_v_free = bar_v_full + NV;
   uint64_t* bar_s_full = bar_v_free + NV;   // [2]
   uint64_t* bar_ds_full = bar_s_full + 2;   // [2]
-  uint64_t* bar_s_free = bar_ds_full + 2;   // [2] dQ has read dS
-  uint64_t* bar_dp_full = bar_s_free + 2;
+  uint64_t* bar_dp_full = bar_ds_full + 2;
   uint64_t* bar_dp_free = bar_dp_full + 1;
   uint64_t* bar_acc_full = bar_dp_free + 1;
   uint64_t* bar_acc_free = bar_acc_full + 1;
@@ -502,7 +502,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; i++) {
       mbar_init(bar_s_full + i, 1);
       mbar_init(bar_ds_full + i, kSoftmax);
-      mbar_init(bar_s_free + i, 1);
       mbar_init(bar_drain + i, 1);
     }
     mbar_init(bar_dp_full, 1);
@@ -557,76 +556,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kSoftmax + 1) {
     regs_dec<64>();
-    // ------------------------------------------------------------ S (and the K tile's tail)
+    // ------------------------------------------------------------ S and dQ
+    // S runs two steps ahead of dQ, over the ends of the items: S(u + 2) goes over dS(u) behind dQ(u), as
+    // products of one thread run in the order of issue.
     const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
+    const uint64_t dKm = sdesc_sw128(smem_u32(smem + PL::kK), 16384, 1024);
     bool ok = true;
+    int us = 0, si = 0, sr = 0, sitems = 0;  // next S: step, step of its item, item
+    QItem is;
+    bool more = q_item(g, a.plan, list_at(0), &is);
+    auto scores = [&]() {
+      if (!more || !ok) return;
+      const int s = us % NK, b = us & 1;
+      if (si == 0) ok = warp_wait(bar_q_full, sitems & 1, abort_flag);
+      if (ok) ok = warp_wait(bar_k_full + s, (us / NK) & 1, abort_flag);
+      if (!ok) return;
+      const int valid = is.end - (is.start + si * 128);
+      if (valid < 128) {
+        // dQ sums over the rows of K
+        zero_tail<D>(smem + PL::kK + s * TB, valid);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        mma_nt<D>(tS + b * 128, dQ, dK + (uint64_t)(s * (TB >> 4)));
+        umma_commit(bar_s_full + b);
+        if (si == is.steps - 1) umma_commit(bar_q_free);
+      }
+      __syncwarp();
+      us++;
+      if (++si == is.steps) {
+        si = 0;
+        sitems++;
+        more = q_item(g, a.plan, list_at(++sr), &is);
+      }
+    };
+    scores();
+    scores();
     int items = 0, u = 0;
     for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
-      ok = warp_wait(bar_q_full, items & 1, abort_flag);
       for (int i = 0; i < it.steps && ok; i++, u++) {
-        const int s = u % NK, b = u & 1;
-        ok = warp_wait(bar_k_full + s, (u / NK) & 1, abort_flag);
-        if (ok && u >= 2) ok = warp_wait(bar_s_free + b, ((u >> 1) - 1) & 1, abort_flag);
+        const int b = u & 1, s = u % NK;
+        ok = warp_wait(bar_ds_full + b, (u >> 1) & 1, abort_flag);
+        if (ok && i == 0 && items > 0) ok = warp_wait(bar_acc_free, (items - 1) & 1, abort_flag);
         if (!ok) break;
-        const int valid = it.end - (it.start + i * 128);
-        if (valid < 128) {
-          // dQ sums over the K rows; it comes after this S, which orders the zeroing before it
-          zero_tail<D>(smem + PL::kK + s * TB, valid);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
         tc_fence_after();
         if (elect_one()) {
-          mma_nt<D>(tS + b * 128, dQ, dK + (uint64_t)(s * (TB >> 4)));
-          umma_commit(bar_s_full + b);
-          if (i == it.steps - 1) umma_commit(bar_q_free);
+          mma_acc<D, 0, 8>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 0);
+          if (i == it.steps - 1) umma_commit(bar_acc_full);
         }
+        __syncwarp();
+        // (K(u + 2) is in flight or there: only K(u + 3) needs the stage of K(u))
+        scores();
+        if (ok && elect_one()) umma_commit(bar_k_free + s);
         __syncwarp();
       }
     }
     drain(bar_drain);
   } else if (warp == kSoftmax + 2) {
     regs_dec<64>();
-    // ------------------------------------------------------------ dP and dQ
+    // ------------------------------------------------------------ dP
     const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
     const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
-    const uint64_t dKm = sdesc_sw128(smem_u32(smem + PL::kK), 16384, 1024);
     bool ok = true;
     int items = 0, u = 0;
     for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
       ok = warp_wait(bar_q_full, items & 1, abort_flag);
-      for (int i = 0; i <= it.steps && ok; i++) {
-        if (i < it.steps) {
-          const int s = u % NV;
-          ok = warp_wait(bar_v_full + s, (u / NV) & 1, abort_flag);
-          if (ok && u > 0) ok = warp_wait(bar_dp_free, (u - 1) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            mma_nt<D>(tP, dG, dV + (uint64_t)(s * (TB >> 4)));
-            umma_commit(bar_dp_full);
-            umma_commit(bar_v_free + s);
-            if (i == it.steps - 1) umma_commit(bar_q_free);
-          }
-          __syncwarp();
+      for (int i = 0; i < it.steps && ok; i++, u++) {
+        const int s = u % NV;
+        ok = warp_wait(bar_v_full + s, (u / NV) & 1, abort_flag);
+        if (ok && u > 0) ok = warp_wait(bar_dp_free, (u - 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_nt<D>(tP, dG, dV + (uint64_t)(s * (TB >> 4)));
+          umma_commit(bar_dp_full);
+          umma_commit(bar_v_free + s);
+          if (i == it.steps - 1) umma_commit(bar_q_free);
         }
-        if (i > 0) {  // dQ of step i - 1
-          const int v = u - 1, b = v & 1, s = v % NK;
-          ok = warp_wait(bar_ds_full + b, (v >> 1) & 1, abort_flag);
-          if (ok && i == 1 && items > 0) ok = warp_wait(bar_acc_free, (items - 1) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            mma_acc<D, 0, 8>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 1);
-            umma_commit(bar_k_free + s);
-            umma_commit(bar_s_free + b);
-          }
-          __syncwarp();
-        }
-        if (i < it.steps) u++;
+        __syncwarp();
       }
-      if (ok && elect_one()) umma_commit(bar_acc_full);
-      __syncwarp();
     }
     drain(bar_drain + 1);
   } else if (warp == kSoftmax + 3) {
