@@ -145,6 +145,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+    tma_prefetch_map(&tmG);
     mbar_init(bar_kv_full, 1);
     mbar_init(bar_kv_free, 1);
     for (int s = 0; s < NS; s++) {
@@ -489,6 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+    tma_prefetch_map(&tmG);
     mbar_init(bar_q_full, 1);
     mbar_init(bar_q_free, 2);
     for (int s = 0; s < NK; s++) {

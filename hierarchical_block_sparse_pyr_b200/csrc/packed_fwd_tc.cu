@@ -93,6 +93,9 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
     for (int i = 0; i < 2; i++) {
       mbar_init(bar_q_full + i, 1);
       mbar_init(bar_q_free + i, 1);

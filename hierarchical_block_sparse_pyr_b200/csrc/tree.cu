@@ -16,27 +16,31 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, T
   tree_prefix(g, a, s_pre, warp_sums);
   const TreeStream ts(g, s_pre);
   const int b = blockIdx.x / ts.HR, hr = blockIdx.x - b * ts.HR;
-  const int64_t nt = s_pre[b + 1] - s_pre[b], first = (int64_t)s_pre[b] * ts.HR + hr * nt;
+  const int nt = s_pre[b + 1] - s_pre[b], first = ts.start(b) + hr * (nt + ts.cost);
   // first and last CTA of the segment
-  int c0 = (int)(first * ts.C / ts.total), c1 = (int)((first + nt - 1) * ts.C / ts.total);
-  while (c0 > 0 && ts.cut(c0) > first) c0--;
-  while (ts.cut(c0 + 1) <= first) c0++;
-  while (c1 > 0 && ts.cut(c1) > first + nt - 1) c1--;
-  while (ts.cut(c1 + 1) <= first + nt - 1) c1++;
+  const int c0 = first / ts.per, c1 = (nt == 1 ? first : first + ts.cost + nt - 1) / ts.per;
+  // the parts are written by the kernel before, which may still run. Every block waits, so that this kernel
+  // cannot end, and what follows it start, before that one has ended
+  grid_wait();
   if (c0 == c1) return;
-  const int slot0 = ts.cut(c0) < first ? 1 : 0;  // the first CTA may hold another segment's end before it
   const int hk = hr / g.RG, rg = hr - hk * g.RG;
   const int rr = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   int hg, t;
   if (rr >= g.RR || !tree_row(g, rg, rr, &hg, &t)) return;
   const int n = c1 - c0 + 1;
-  auto part = [&](int i) { return (int64_t)((c0 + i) * 2 + (i == 0 ? slot0 : 0)) * g.RR + rr; };
+  auto part = [&](int i) { return ((int64_t)(c0 + i) * 2 + (i == 0)) * g.RR + rr; };
+  constexpr int E = D / 32;
+  constexpr int kAhead = 8;  // parts fetched before their weights are known
+  float ahead[kAhead][E];
+#pragma unroll
+  for (int i = 0; i < kAhead; i++)
+#pragma unroll
+    for (int e = 0; e < E; e++) ahead[i][e] = i < n ? a.part_o[part(i) * D + lane * E + e] : 0.f;
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_ml[2 * part(i)]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float mu = m == -INFINITY ? 0.f : m;
-  constexpr int E = D / 32;
   float acc[E] = {}, l = 0.f;
   for (int base = 0; base < n; base += 32) {
     float w = 0.f;
@@ -45,9 +49,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, T
       w = exp2f(ml.x - mu);
       l += w * ml.y;
     }
+    if (base == 0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+        for (int e = 0; e < E; e++) acc[e] = fmaf(wi, ahead[i][e], acc[e]);
+      }
+    }
     const int cnt = min(32, n - base);
 #pragma unroll 4
-    for (int i = 0; i < cnt; i++) {
+    for (int i = base ? 0 : kAhead; i < cnt; i++) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const float* p = a.part_o + part(base + i) * D + lane * E;
 #pragma unroll
@@ -70,8 +82,18 @@ cudaError_t launch_join(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
   const int used = g.HM ? g.G * g.T <= 128 ? g.G * g.T : g.RR : g.G * g.T;
   const int rows = used < g.RR ? used : g.RR;
   const dim3 grid(g.B * g.Hkv * g.RG, (rows + kJoinWarps - 1) / kJoinWarps);
-  tree_join_kernel<T, D><<<grid, kJoinWarps * 32, (g.B + 1) * sizeof(int), st>>>(g, a);
-  return cudaGetLastError();
+  // launched while the kernel before it still runs; it works out its segments and then waits for the parts
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = (g.B + 1) * sizeof(int);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, g, a);
 }
 
 int make_tree_geo(const tree_shape* s, TreeGeo* g) {
@@ -94,9 +116,8 @@ int make_tree_geo(const tree_shape* s, TreeGeo* g) {
     t.C = 296;  // two CTAs per SM
     t.RG = (t.G * t.T + t.RR - 1) / t.RR;
   }
-  if ((int64_t)t.B * (((int64_t)t.N + t.BK - 1) / t.BK) > 0x7fffffff ||
-      (int64_t)t.B * t.Hkv * t.RG > 0x7fffffff)
-    return PYR_EUNSUPPORTED;
+  // positions of the stream are 32-bit
+  if ((((int64_t)t.N + t.BK - 1) / t.BK + kSegCost) * t.B > 0x7fffffff / t.Hkv / t.RG - t.C) return PYR_EUNSUPPORTED;
   *g = t;
   return PYR_OK;
 }

@@ -5,6 +5,11 @@
 
 namespace pyr {
 
+// Overlap of two kernels of a stream: the second may start once every block of the first has called
+// grid_launch (or has ended), and waits in grid_wait until the first has ended and its writes are visible.
+__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Rows of a unit (sequence, key/value head): drafted token t of the group's head h. They are cut into row
 // groups of RR rows, and the keys into tiles of BK. On the CUDA cores (HM = 0) row r = h * T + t is row
 // r % RR of group r / RR; on the tensor cores a group is RR / 128 tiles that hold the T rows of HM heads each.
@@ -53,35 +58,74 @@ __device__ __forceinline__ int tree_tiles(const TreeGeo& g, const TreeArgs& a, i
   return tree_len(g, a, b, &n) ? (n + g.T + g.BK - 1) / g.BK : 1;
 }
 
-// The tiles of all (sequence, unit, row group) in that order form one stream; CTA c < C takes the positions
-// [cut(c), cut(c + 1)), at least one, whatever segments they fall in. pre[b] = tiles of one row group of
-// the sequences before b (in shared memory, B + 1 entries).
+// The tiles of all segments (sequence, unit, row group) in that order form one stream, which is cut into C
+// equal shares. A segment costs its tiles and, for its queries, masks and epilogue, about kSegCost tiles
+// more: positions 0 .. nt + cost - 1, tile 0 at position 0 and tile t > 0 at position cost + t. (Measured on
+// 4 sequences of 511 to 32000 tokens, 64 drafts: without the cost, CTAs that got the short sequences ran 1.7
+// times as long as the others.) The cost counts only if a share is longer than it, so that every CTA between
+// the first and the last of a segment has a tile of it.
+constexpr int kSegCost = 3, kSegCostFrom = 8;  // tiles; from this many tiles a CTA on
+
 struct TreeStream {
-  const int* pre;
-  int B, HR;  // HR: row groups of a sequence
-  int64_t total;
-  int C;
-  __device__ TreeStream(const TreeGeo& g, const int* p)
-      : pre(p), B(g.B), HR(g.Hkv * g.RG), total((int64_t)p[g.B] * g.Hkv * g.RG), C(total < g.C ? (int)total : g.C) {}
-  __device__ int64_t cut(int c) const { return total / C * c + total % C * c / C; }
-  // the segment that holds position x: sequence, unit and row group, first position, tiles
-  __device__ void find(int64_t x, int* b, int* hr, int64_t* first, int* tiles) const {
+  const int* pre;  // tiles of one row group of the sequences before b (shared memory, B + 1 entries)
+  int B, HR;       // HR: row groups of a sequence
+  int cost, total, per;  // positions of a segment beyond its tiles, of the stream, of a CTA
+  __device__ TreeStream(const TreeGeo& g, const int* p) : pre(p), B(g.B), HR(g.Hkv * g.RG) {
+    const int tiles = p[g.B] * HR;
+    cost = tiles >= kSegCostFrom * g.C ? kSegCost : 0;
+    total = tiles + g.B * HR * cost;
+    per = (total + g.C - 1) / g.C;
+  }
+  __device__ int start(int b) const { return (pre[b] + b * cost) * HR; }
+  // the segment that holds position x: sequence, row group, first position, tiles
+  __device__ void find(int x, int* b, int* hr, int* first, int* tiles) const {
     int lo = 0, hi = B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((int64_t)pre[mid] * HR <= x)
+      if (start(mid) <= x)
         lo = mid;
       else
         hi = mid;
     }
-    const int nt = pre[lo + 1] - pre[lo];
-    const int64_t at = (int64_t)pre[lo] * HR;
+    const int nt = pre[lo + 1] - pre[lo], at = start(lo);
     *b = lo;
-    *hr = (int)((x - at) / nt);
-    *first = at + (int64_t)*hr * nt;
+    *hr = (x - at) / (nt + cost);
+    *first = at + *hr * (nt + cost);
     *tiles = nt;
   }
 };
+
+// A CTA's pieces of segments, in stream order.
+struct TreePiece {
+  int b, hk, rg, len;
+  int t0, steps;  // first tile, tiles
+  bool good;      // the sequence's length is in range
+  bool whole;     // the CTA holds the whole segment
+  int part;       // else: which of the CTA's two parts this is. 0 continues a segment, 1 begins one
+  int next;       // position behind the segment
+};
+
+// the first piece with tiles at or behind position x of a CTA whose share ends at x1
+__device__ __forceinline__ bool tree_piece(const TreeGeo& g, const TreeArgs& a, const TreeStream& ts, int x, int x1,
+                                           TreePiece* p) {
+  for (; x < x1; x = p->next) {
+    int hr, first, tiles;
+    ts.find(x, &p->b, &hr, &first, &tiles);
+    p->next = first + tiles + ts.cost;
+    p->t0 = x == first ? 0 : max(1, x - first - ts.cost);
+    const int t1 = x1 >= p->next ? tiles : max(p->t0 == 0 ? 1 : p->t0, x1 - first - ts.cost);
+    p->steps = t1 - p->t0;
+    if (p->steps <= 0) continue;
+    p->hk = hr / g.RG;
+    p->rg = hr - p->hk * g.RG;
+    p->whole = p->t0 == 0 && t1 == tiles;
+    p->part = p->t0 == 0;
+    p->good = tree_len(g, a, p->b, &p->len);
+    if (!p->good) p->len = 0;
+    return true;
+  }
+  return false;
+}
 
 // pre[0 .. B] by the whole block (blockDim.x a multiple of 32, at most 1024); warp_sums: 32 ints
 __device__ __forceinline__ void tree_prefix(const TreeGeo& g, const TreeArgs& a, int* pre, int* warp_sums) {

@@ -22,20 +22,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
   int* pre = reinterpret_cast<int*>(Vs + kTile * D);
   __shared__ int warp_sums[32];
   __shared__ TreeMaskBuf masks;
+  grid_launch();
   tree_prefix(g, a, pre, warp_sums);
   const TreeStream ts(g, pre);
-  if (blockIdx.x >= ts.C) return;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float sl2 = rsqrtf((float)D) * 1.4426950408889634f;
-  const int64_t x0 = ts.cut(blockIdx.x), x1 = ts.cut(blockIdx.x + 1);
-  for (int64_t x = x0; x < x1;) {
-    int b, hr, tiles, len;
-    int64_t first;
-    ts.find(x, &b, &hr, &first, &tiles);
-    const int t0 = (int)(x - first), t1 = (int)(x1 - first < tiles ? x1 - first : tiles);
-    const int hk = hr / g.RG, r0 = (hr - hk * g.RG) * g.RR;
-    const bool good = tree_len(g, a, b, &len);
-    if (!good) len = 0;
+  const int x1 = min((blockIdx.x + 1) * ts.per, ts.total);
+  TreePiece pc;
+  for (int x = blockIdx.x * ts.per; tree_piece(g, a, ts, x, x1, &pc); x = pc.next) {
+    const int b = pc.b, hk = pc.hk, len = pc.len, t0 = pc.t0, t1 = pc.t0 + pc.steps, r0 = pc.rg * g.RR;
+    const bool good = pc.good;
     __syncthreads();
     if (threadIdx.x < 32) tree_masks(g, a, b, good, &masks);
     const int nr = min(kTile, g.G * g.T - r0);
@@ -81,8 +77,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
       __syncwarp();
       mul_acc<D>(acc, Ps, Vs, D);
     }
-    const bool whole = t0 == 0 && t1 == tiles;
-    const int64_t part = (int64_t)(blockIdx.x * 2 + (x == x0 ? 0 : 1)) * g.RR;
+    const bool whole = pc.whole;
+    const int64_t part = (int64_t)(blockIdx.x * 2 + pc.part) * g.RR;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int r = 4 * ty + i;
@@ -98,7 +94,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
         if (tx == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (part + r)) = make_float2(m[i], l[i]);
       }
     }
-    x = first + t1;
   }
 }
 

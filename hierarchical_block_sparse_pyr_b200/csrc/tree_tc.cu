@@ -40,30 +40,18 @@ struct TPlan {
   static constexpr int kBytes = kPre + 1024;  // + 4 (B + 1)
 };
 
-// a CTA's piece of a segment
-struct Seg {
-  int b, hk, rg, len, t0, steps;
-  bool good, whole, first;
-  int64_t next;
-};
-
-__device__ __forceinline__ void seg_at(const TreeGeo& g, const TreeArgs& a, const TreeStream& ts, int64_t x, int64_t x0,
-                                       int64_t x1, Seg* s) {
-  int hr, tiles;
-  int64_t at;
-  ts.find(x, &s->b, &hr, &at, &tiles);
-  s->b = uniform(s->b);
-  hr = uniform(hr);
-  s->hk = hr / g.RG;
-  s->rg = hr - s->hk * g.RG;
-  s->t0 = uniform((int)(x - at));
-  const int t1 = (int)(x1 - at < tiles ? x1 - at : tiles);
-  s->steps = uniform(t1 - s->t0);
-  s->whole = s->t0 == 0 && t1 == tiles;
-  s->first = x == x0;
-  s->next = at + t1;
-  s->good = uniform(tree_len(g, a, s->b, &s->len));
-  s->len = s->good ? uniform(s->len) : 0;
+// a piece, with what the issuing warps take from it in uniform registers
+__device__ __forceinline__ bool piece_at(const TreeGeo& g, const TreeArgs& a, const TreeStream& ts, int x, int x1,
+                                         TreePiece* p) {
+  if (!uniform(tree_piece(g, a, ts, x, x1, p))) return false;
+  p->b = uniform(p->b);
+  p->hk = uniform(p->hk);
+  p->rg = uniform(p->rg);
+  p->len = uniform(p->len);
+  p->t0 = uniform(p->t0);
+  p->steps = uniform(p->steps);
+  p->next = uniform(p->next);
+  return true;
 }
 
 // bit c: key u0 + c, counted from the first drafted token, is visible to a row with this (non-zero) mask
@@ -104,6 +92,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
     mbar_init(bar_q_full, 1);
     mbar_init(bar_q_free, 1);
     for (int s = 0; s < NS; s++) {
@@ -125,9 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     *abort_flag = 0;
   }
+  grid_launch();
   tree_prefix(g, a, pre, reinterpret_cast<int*>(smem + PL::kSums));
   const TreeStream ts(g, pre);
-  if (blockIdx.x >= ts.C) return;
+  const int x0 = blockIdx.x * ts.per, x1 = min(x0 + ts.per, ts.total);
+  if (x0 >= x1) return;
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -139,16 +132,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS = tmem, tO = tmem + 256;
   unsigned char* sQ = smem + PL::kQ;
   unsigned char* ring = smem + PL::kRing;
-  const int64_t x0 = ts.cut(blockIdx.x), x1 = ts.cut(blockIdx.x + 1);
-  Seg sg;
+  TreePiece sg;
 
   if (warp == 8) {
     regs_dec<88>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int u = 0, segs = 0;
-    for (int64_t x = x0; x < x1 && ok; x = sg.next) {
-      seg_at(g, a, ts, x, x0, x1, &sg);
+    for (int x = x0; ok && piece_at(g, a, ts, x, x1, &sg); x = sg.next) {
       auto load = [&](const CUtensorMap* map, int t) {
         const int s = u % NS, k = u / NS;
         if (k > 0 && ok) ok = warp_wait(bar_free + s, (k - 1) & 1, abort_flag);
@@ -190,8 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
     bool ok = true;
     int u = 0, segs = 0, ns[2] = {0, 0};
-    for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
-      seg_at(g, a, ts, x, x0, x1, &sg);
+    for (int x = x0; ok && piece_at(g, a, ts, x, x1, &sg); x = sg.next, segs++) {
       for (int i = 0; i < sg.steps && ok; i++, u += 2) {
         const int s = u % NS;
         ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
@@ -228,8 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
     bool ok = true;
     int u = 1, segs = 0, np[2] = {0, 0}, no[2] = {0, 0};
-    for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
-      seg_at(g, a, ts, x, x0, x1, &sg);
+    for (int x = x0; ok && piece_at(g, a, ts, x, x1, &sg); x = sg.next, segs++) {
       unsigned long long used = 0;
       ok = warp_wait(bar_m_full + (segs & 1), (segs >> 1) & 1, abort_flag);
       if (!ok) break;
@@ -286,8 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ masks
     bool ok = true;
     int segs = 0;
-    for (int64_t x = x0; x < x1; x = sg.next, segs++) {
-      seg_at(g, a, ts, x, x0, x1, &sg);
+    for (int x = x0; piece_at(g, a, ts, x, x1, &sg); x = sg.next, segs++) {
       if (segs >= 2) ok = warp_wait(bar_m_free + (segs & 1), ((segs >> 1) - 1) & 1, abort_flag);
       if (!ok) break;
       tree_masks(g, a, sg.b, sg.good, masks + (segs & 1));
@@ -305,8 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hl = rt / g.T, tok = rt - hl * g.T;
     bool ok = true;
     int n = 0, n1 = 0, segs = 0, twos = 0;  // so far: S tiles of this slot, of slot 1, segments, with two slots
-    for (int64_t x = x0; x < x1 && ok; x = sg.next, segs++) {
-      seg_at(g, a, ts, x, x0, x1, &sg);
+    for (int x = x0; ok && piece_at(g, a, ts, x, x1, &sg); x = sg.next, segs++) {
       const int hg = (sg.rg * MT + (SPLIT ? 0 : sl)) * g.HM + hl;  // head of the group
       const bool row_ok = hl < g.HM && hg < g.G;
       ok = warp_wait(bar_m_full + (segs & 1), (segs >> 1) & 1, abort_flag);
@@ -426,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int head = sg.hk * g.G + hg;
       const int64_t part =
-          (int64_t)(blockIdx.x * 2 + (sg.first ? 0 : 1)) * g.RR + (SPLIT ? 0 : sl) * 128 + rt;
+          (int64_t)(blockIdx.x * 2 + sg.part) * g.RR + (SPLIT ? 0 : sl) * 128 + rt;
       if (sg.whole) {
         const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
         w0 *= inv;
