@@ -31,7 +31,8 @@ struct TPlan {
   static constexpr int kQ = 0;
   static constexpr int kRing = MT * TB;
   static constexpr int kMasks = kRing + NS * TB;  // [2]
-  static constexpr int kMl = kMasks + 2 * (int)sizeof(TreeMaskBuf);  // [128][2] fp32: slot 1's maximum and sum
+  static constexpr int kPieces = kMasks + 2 * (int)sizeof(TreeMaskBuf);  // [2], with the masks
+  static constexpr int kMl = kPieces + 2 * 64;  // [128][2] fp32: slot 1's maximum and sum
   static constexpr int kBar = kMl + 1024;
   static constexpr int kNumBars = 2 + 2 * NS + 2 + 4 + 2 + 2 + 4 + 2 + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
   TreeMaskBuf* masks = reinterpret_cast<TreeMaskBuf*>(smem + PL::kMasks);
+  TreePiece* pieces = reinterpret_cast<TreePiece*>(smem + PL::kPieces);
   float2* ml = reinterpret_cast<float2*>(smem + PL::kMl);
   int* pre = reinterpret_cast<int*>(smem + PL::kPre);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -273,12 +275,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 11) {
     regs_dec<88>();
     // ------------------------------------------------------------ masks
-    bool ok = true;
+    // (and the pieces, so that the softmax warps need not hold more of them than they use)
+    bool more = true;
     int segs = 0;
-    for (int x = x0; piece_at(g, a, ts, x, x1, &sg); x = sg.next, segs++) {
-      if (segs >= 2) ok = warp_wait(bar_m_free + (segs & 1), ((segs >> 1) - 1) & 1, abort_flag);
-      if (!ok) break;
-      tree_masks(g, a, sg.b, sg.good, masks + (segs & 1));
+    for (int x = x0; more; x = sg.next, segs++) {
+      more = piece_at(g, a, ts, x, x1, &sg);
+      if (segs >= 2 && !warp_wait(bar_m_free + (segs & 1), ((segs >> 1) - 1) & 1, abort_flag)) break;
+      if (more)
+        tree_masks(g, a, sg.b, sg.good, masks + (segs & 1));
+      else
+        sg.steps = 0;
+      if (lane == 0) pieces[segs & 1] = sg;
+      __syncwarp();
       if (lane == 0) mbar_arrive(bar_m_full + (segs & 1));
     }
   } else {
@@ -293,17 +301,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hl = rt / g.T, tok = rt - hl * g.T;
     bool ok = true;
     int n = 0, n1 = 0, segs = 0, twos = 0;  // so far: S tiles of this slot, of slot 1, segments, with two slots
-    for (int x = x0; ok && piece_at(g, a, ts, x, x1, &sg); x = sg.next, segs++) {
-      const int hg = (sg.rg * MT + (SPLIT ? 0 : sl)) * g.HM + hl;  // head of the group
-      const bool row_ok = hl < g.HM && hg < g.G;
+    for (;; segs++) {
       ok = warp_wait(bar_m_full + (segs & 1), (segs >> 1) & 1, abort_flag);
       if (!ok) break;
+      const TreePiece* pc = pieces + (segs & 1);
+      const int steps = uniform(pc->steps);
+      if (steps == 0) break;
+      // head of the group this row belongs to
+      const bool row_ok = hl < g.HM && (pc->rg * MT + (SPLIT ? 0 : sl)) * g.HM + hl < g.G;
       const unsigned long long mask = row_ok ? masks[segs & 1].mask[tok] : 0ull;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_m_free + (segs & 1));
       const bool live = __any_sync(0xffffffffu, mask != 0);
+      // first key of the next tile, counted from the first drafted token
+      int v0 = ((pc->t0 + (SPLIT ? sl : 0)) * 128) - pc->len;
       float m_ref = -INFINITY, l_sum = 0.f;
-      for (int i = SPLIT ? sl : 0; i < sg.steps; i += SPLIT ? 2 : 1, n++) {
+      for (int i = SPLIT ? sl : 0; i < steps; i += SPLIT ? 2 : 1, n++, v0 += SPLIT ? 256 : 128) {
         ok = warp_wait(bar_s_full + sl, n & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -315,17 +326,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
-        const int k0 = (sg.t0 + i) * 128;
         float s[128];
 #pragma unroll
         for (int c = 0; c < 128; c += 32) tmem_ld32(tS_row + c, s + c);
         tmem_wait_ld();
-        if (k0 + 128 > sg.len) {
-          const unsigned long long v0 = visible64(k0 - sg.len, mask), v1 = visible64(k0 + 64 - sg.len, mask);
+        if (v0 > -128) {
+          const unsigned long long m0 = visible64(v0, mask), m1 = visible64(v0 + 64, mask);
 #pragma unroll
           for (int c = 0; c < 64; c++) {
-            s[c] = (v0 >> c) & 1 ? s[c] : -INFINITY;
-            s[c + 64] = (v1 >> c) & 1 ? s[c + 64] : -INFINITY;
+            s[c] = (m0 >> c) & 1 ? s[c] : -INFINITY;
+            s[c + 64] = (m1 >> c) & 1 ? s[c + 64] : -INFINITY;
           }
         }
         const float mx = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
@@ -380,8 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_ref = -INFINITY;
         l_sum = 0.f;
       }
-      const bool two = SPLIT && sg.steps > 1;  // slot 1 has part of the keys
+      const bool two = SPLIT && steps > 1;  // slot 1 has part of the keys
       if (SPLIT && sl == 1) {
+        if (lane == 0) mbar_arrive(bar_m_free + (segs & 1));
         if (!two) continue;
         if (twos > 0) ok = warp_wait(bar_ml_free, (twos - 1) & 1, abort_flag);
         if (!ok) break;
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(bar_pv + sl, (n - 1) & 1, abort_flag);
       float w0 = 1.f, w1 = 0.f;
       if (two) {
-        n1 += sg.steps >> 1;
+        n1 += steps >> 1;
         if (ok) ok = warp_wait(bar_ml_full, twos & 1, abort_flag);
         if (ok) ok = warp_wait(bar_pv + 1, (n1 - 1) & 1, abort_flag);
         if (!ok) break;
@@ -411,10 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       tc_fence_after();
-      const int head = sg.hk * g.G + hg;
+      const int b = pc->b, hg = (pc->rg * MT + (SPLIT ? 0 : sl)) * g.HM + hl, head = pc->hk * g.G + hg;
+      const bool whole = pc->whole;
       const int64_t part =
-          (int64_t)(blockIdx.x * 2 + sg.part) * g.RR + (SPLIT ? 0 : sl) * 128 + rt;
-      if (sg.whole) {
+          (int64_t)(blockIdx.x * 2 + pc->part) * g.RR + (SPLIT ? 0 : sl) * 128 + rt;
+      if (whole) {
         const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
         w0 *= inv;
         w1 *= inv;
@@ -438,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 32; k++) o[k] = seen ? o[k] : 0.f;
-        if (row_ok && sg.whole) {
-          store32_bf16(view_at<__nv_bfloat16>(a.o, sg.b, head, tok) + c, o, 1.f);
+        if (row_ok && whole) {
+          store32_bf16(view_at<__nv_bfloat16>(a.o, b, head, tok) + c, o, 1.f);
         } else if (row_ok) {
           float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c);
 #pragma unroll
@@ -449,12 +461,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
+        mbar_arrive(bar_m_free + (segs & 1));
         mbar_arrive(bar_o_free + sl);
         if (two) mbar_arrive(bar_o_free + 1);
       }
-      if (row_ok && sg.whole) {
+      if (row_ok && whole) {
         if (a.lse)
-          a.lse[((int64_t)sg.b * g.Hq + head) * g.T + tok] =
+          a.lse[((int64_t)b * g.Hq + head) * g.T + tok] =
               l_sum > 0.f ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
       } else if (row_ok) {
         *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_sum);
