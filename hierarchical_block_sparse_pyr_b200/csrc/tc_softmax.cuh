@@ -109,6 +109,16 @@ __device__ __forceinline__ float2 exp2_mix(int c, float2 x) {
   return make_float2(ex2(x.x), ex2(x.y));
 }
 
+// Two softmax warps of a scheduler take turns with their exponentials, so that the one's run while the
+// other's products do; left alone, both end up waiting for the tensor cores, and then for the MUFU unit, at
+// the same time. A turn is a hint: it is not waited for longer than a step takes.
+__device__ __forceinline__ void turn_wait(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 < 4096) {
+  }
+  __syncwarp();
+}
+
 // position in a work list of a persistent CTA's r-th item: the lists are sorted by work, and going back and
 // forth over the CTAs evens out their sums
 __device__ __forceinline__ int64_t list_at(int r) {
