@@ -19,10 +19,10 @@ struct PackedGeo {
 constexpr int kPlanHeader = 16;
 constexpr int kListFwd = 0, kListQ = 1, kListK = 2;
 
-// tokens per tile of a list. fp32: 64. bf16: 128, and in the forward pass 256 where the two 128-row tiles of
+// tokens per tile of a list. fp32: 32 (packed_simt.cu). bf16: 128, and in the forward pass 256 where the two 128-row tiles of
 // a CTA come from one head (packed_fwd_tc.cu).
 __host__ __device__ inline int packed_tile_rows(const PackedGeo& g, int list) {
-  if (g.dtype == PYR_F32) return 64;
+  if (g.dtype == PYR_F32) return 32;
   return list == kListFwd && g.G % 2 ? 256 : 128;
 }
 

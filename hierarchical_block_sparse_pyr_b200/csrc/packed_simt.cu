@@ -1,10 +1,10 @@
 // Causal attention of packed prompts and its gradients on the CUDA cores, fp32 arithmetic throughout: the
 // fp32 path (reduced-precision tensor-core operands would lose what fp32 callers keep).
 //
-// Forward and dQ: one CTA per (64-row tile, query head), walking the keys up to the tile's end. dK/dV: one
-// CTA per (64-key tile, key/value head), walking the rows from the tile's start on, over the heads of its
-// group, so that every gradient is summed by one CTA in a fixed order. Tiles come longest first from the
-// plan. Rows behind the sequence's end are loaded as zeros, never from memory.
+// Forward and dQ: one CTA of 128 threads per (32-row tile, query head), walking the keys up to the tile's end.
+// dK/dV: one per (32-key tile, key/value head), walking the rows from the tile's start on, over the heads of
+// its group, so that every gradient is summed by one CTA in a fixed order. Tiles come longest first from the
+// plan. 32 rows rather than 64: a CTA's walk is the longest chain of the call, and two to five CTAs share an SM. Rows behind the sequence's end are loaded as zeros, never from memory.
 #include "packed.cuh"
 #include "simt_tile.cuh"
 
@@ -15,25 +15,27 @@ namespace {
 using namespace simt;
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kRows = 32;  // rows of a tile, packed_tile_rows() of fp32
+constexpr int kThreads = 4 * kRows;
 
 template <int D>
 constexpr int fwd_smem() {
-  return (2 * kTile * (D + 4) + kTile * D) * 4;  // Q, K (P over K), V
+  return ((kRows + kTile) * (D + 4) + kTile * D) * 4;  // Q, K (P over K), V
 }
 
 // S = Q K^T, online softmax, O += P V over 64-key tiles; P goes over K's buffer.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
+__global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float *Qs = sm, *Ks = Qs + kTile * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
+  float *Qs = sm, *Ks = Qs + kRows * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
   if (tile >= a.plan[kListFwd]) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListFwd))[tile];
   const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float sl2 = rsqrtf((float)D) * kLog2e;
-  const int nrow = min(kTile, end - row0);
-  load_rows<T, D>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  const int nrow = min(kRows, end - row0);
+  load_rows<T, D, kRows>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
   float m[4], l[4], acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -46,8 +48,8 @@ __global__ void __launch_bounds__(kThreads, 2) packed_fwd_simt_kernel(PackedGeo 
   for (int k0 = start; k0 < stop; k0 += kTile) {
     const int nk = min(kTile, stop - k0);
     __syncthreads();
-    load_rows<T, D>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
-    load_rows<T, D>(Vs, D, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    load_rows<T, D, kTile>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<T, D, kTile>(Vs, D, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
     __syncthreads();
     float s[4][4];
     mul_nt<D>(s, Qs, D + 4, Ks, D + 4);
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(PackedGeo g, PackedBw
 
 template <int D>
 constexpr int dq_smem() {
-  return (4 * kTile * (D + 4) + kTile * kPitchP) * 4;  // Q, dO, K, V, dS
+  return (2 * (kRows + kTile) * (D + 4) + kRows * kPitchP) * 4;  // two operands each way, P or dS
 }
 
 // dS = P (dO V^T - delta), dQ += dS K
@@ -100,16 +102,16 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
-  float *Qs = sm, *Gs = Qs + kTile * P, *Ks = Gs + kTile * P, *Vs = Ks + kTile * P, *Ps = Vs + kTile * P;
+  float *Qs = sm, *Gs = Qs + kRows * P, *Ks = Gs + kRows * P, *Vs = Ks + kTile * P, *Ps = Vs + kTile * P;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
   if (tile >= a.plan[kListQ]) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
   const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
-  const int nrow = min(kTile, end - row0);
-  load_rows<T, D>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
-  load_rows<T, D>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
+  const int nrow = min(kRows, end - row0);
+  load_rows<T, D, kRows>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<T, D, kRows>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
   float lse2[4], del[4], acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -123,8 +125,8 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
   for (int k0 = start; k0 < stop; k0 += kTile) {
     const int nk = min(kTile, stop - k0);
     __syncthreads();
-    load_rows<T, D>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
-    load_rows<T, D>(Vs, P, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    load_rows<T, D, kTile>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<T, D, kTile>(Vs, P, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
     __syncthreads();
     float s[4][4], dp[4][4];
     mul_nt<D>(s, Qs, P, Ks, P);
@@ -149,16 +151,16 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
-  float *Ks = sm, *Vs = Ks + kTile * P, *Qs = Vs + kTile * P, *Gs = Qs + kTile * P, *Ps = Gs + kTile * P;
+  float *Ks = sm, *Vs = Ks + kRows * P, *Qs = Vs + kRows * P, *Gs = Qs + kTile * P, *Ps = Gs + kTile * P;
   const int tile = blockIdx.x / g.Hkv, hk = blockIdx.x - tile * g.Hkv;
   if (tile >= a.plan[kListK]) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListK))[tile];
   const int end = w.y, key0 = w.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
-  const int nk = min(kTile, end - key0);
-  load_rows<T, D>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
-  load_rows<T, D>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
+  const int nk = min(kRows, end - key0);
+  load_rows<T, D, kRows>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
+  load_rows<T, D, kRows>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
   float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++)
@@ -168,8 +170,8 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g,
     for (int q0 = key0; q0 < end; q0 += kTile) {
       const int nq = min(kTile, end - q0);
       __syncthreads();
-      load_rows<T, D>(Qs, P, view_at<T>(a.q, 0, h, q0), a.q.row, nq);
-      load_rows<T, D>(Gs, P, view_at<T>(a.dout, 0, h, q0), a.dout.row, nq);
+      load_rows<T, D, kTile>(Qs, P, view_at<T>(a.q, 0, h, q0), a.q.row, nq);
+      load_rows<T, D, kTile>(Gs, P, view_at<T>(a.dout, 0, h, q0), a.dout.row, nq);
       __syncthreads();
       float s[4][4], dp[4][4];
       mul_nt<D>(s, Ks, P, Qs, P);

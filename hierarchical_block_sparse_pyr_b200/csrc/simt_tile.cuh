@@ -1,7 +1,7 @@
-// 64 x 64 tiles of fp32 attention on the CUDA cores, 256 threads. Thread (tx, ty) = (tid % 16, tid / 16)
-// owns rows 4 ty .. 4 ty + 3 of every product; of a 64 x 64 product it owns the columns tx + 16 j (four,
+// ROWS x 64 tiles of fp32 attention on the CUDA cores, 4 ROWS threads. Thread (tx, ty) = (tid % 16, tid / 16)
+// owns rows 4 ty .. 4 ty + 3 of every product; of a ROWS x 64 product it owns the columns tx + 16 j (four,
 // which keeps the 16-byte reads of the other operand's rows conflict-free with a row pitch of D + 4), of a
-// 64 x D product the columns 4 tx + 64 j .. + 3.
+// ROWS x D product the columns 4 tx + 64 j .. + 3. Rows of the result are written and read by one half-warp.
 #pragma once
 
 #include "view.cuh"
@@ -9,15 +9,14 @@
 namespace pyr {
 namespace simt {
 
-constexpr int kTile = 64;
-constexpr int kThreads = 256;
+constexpr int kTile = 64;            // columns of a step
 constexpr int kPitchP = kTile + 4;
 
-// dst[r][0 .. D) = row r of src where wanted(r), zeros in the other of the 64 rows
-template <typename T, int D, typename F>
+// dst[r][0 .. D) = row r of src where wanted(r), zeros in the other of the N rows
+template <typename T, int D, int N, typename F>
 __device__ __forceinline__ void load_rows_if(float* dst, int pitch, const T* src, int64_t stride, F wanted) {
   constexpr int E = 16 / sizeof(T), C = D / E;
-  for (int x = threadIdx.x; x < kTile * C; x += kThreads) {
+  for (int x = threadIdx.x; x < N * C; x += blockDim.x) {
     const int r = x / C, c = x - r * C;
     float* d = dst + r * pitch + c * E;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -35,19 +34,20 @@ __device__ __forceinline__ void load_rows_if(float* dst, int pitch, const T* src
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int N>
 __device__ __forceinline__ void load_rows(float* dst, int pitch, const T* src, int64_t stride, int n) {
-  load_rows_if<T, D>(dst, pitch, src, stride, [n](int r) { return r < n; });
+  load_rows_if<T, D, N>(dst, pitch, src, stride, [n](int r) { return r < n; });
 }
 
 // acc[i][j] = A[4 ty + i] . B[tx + 16 j] over D elements
 template <int D>
 __device__ __forceinline__ void mul_nt(float (&acc)[4][4], const float* A, int pa, const float* B, int pb) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  float2 sum[4][4];  // of the even and of the odd elements
 #pragma unroll
   for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int j = 0; j < 4; j++) acc[i][j] = 0.f;
+    for (int j = 0; j < 4; j++) sum[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int e = 0; e < D; e += 4) {
     float4 a[4], b[4];
@@ -59,12 +59,14 @@ __device__ __forceinline__ void mul_nt(float (&acc)[4][4], const float* A, int p
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+        sum[i][j] = __ffma2_rn(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), sum[i][j]);
+        sum[i][j] = __ffma2_rn(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), sum[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++) acc[i][j] = sum[i][j].x + sum[i][j].y;
 }
 
 // acc[i][4 j + c] += sum_k P[4 ty + i][k] V[k][4 tx + 64 j + c], k = 0 .. 63
@@ -86,10 +88,10 @@ __device__ __forceinline__ void mul_acc(float (&acc)[4][D / 16], const float* P,
         const float4 v = *reinterpret_cast<const float4*>(V + (k + kk) * pv + 4 * tx + 64 * j);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          acc[i][4 * j + 0] = fmaf(p[i][kk], v.x, acc[i][4 * j + 0]);
-          acc[i][4 * j + 1] = fmaf(p[i][kk], v.y, acc[i][4 * j + 1]);
-          acc[i][4 * j + 2] = fmaf(p[i][kk], v.z, acc[i][4 * j + 2]);
-          acc[i][4 * j + 3] = fmaf(p[i][kk], v.w, acc[i][4 * j + 3]);
+          float2* c = reinterpret_cast<float2*>(&acc[i][4 * j]);
+          const float2 w = make_float2(p[i][kk], p[i][kk]);
+          c[0] = __ffma2_rn(w, make_float2(v.x, v.y), c[0]);
+          c[1] = __ffma2_rn(w, make_float2(v.z, v.w), c[1]);
         }
       }
   }

@@ -111,7 +111,7 @@ int make_tree_geo(const tree_shape* s, TreeGeo* g) {
     t.RG = (t.G + t.HM * (t.RR / 128) - 1) / (t.HM * (t.RR / 128));
   } else {
     t.HM = 0;
-    t.RR = 64;
+    t.RR = t.G * t.T <= 32 ? 32 : 64;  // more rows share a key tile, fewer waste nothing
     t.BK = 64;
     t.C = 296;  // two CTAs per SM
     t.RG = (t.G * t.T + t.RR - 1) / t.RR;

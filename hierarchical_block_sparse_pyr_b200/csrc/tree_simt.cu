@@ -1,4 +1,4 @@
-// Attention of drafted trees over a cache on the CUDA cores, fp32 arithmetic: 64 rows x 64 keys a step.
+// Attention of drafted trees over a cache on the CUDA cores, fp32 arithmetic: 32 or 64 rows x 64 keys a step.
 // Every CTA walks its share of the stream of tiles (tree.cuh) and writes the rows of a segment itself where
 // it holds the whole segment, else a part for the join.
 #include "simt_tile.cuh"
@@ -10,15 +10,15 @@ namespace {
 
 using namespace simt;
 
-template <int D>
+template <int D, int ROWS>
 constexpr int tree_smem() {
-  return (2 * kTile * (D + 4) + kTile * D) * 4;
+  return ((ROWS + kTile) * (D + 4) + kTile * D) * 4;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeArgs a) {
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float *Qs = sm, *Ks = Qs + kTile * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
+  float *Qs = sm, *Ks = Qs + ROWS * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
   int* pre = reinterpret_cast<int*>(Vs + kTile * D);
   __shared__ int warp_sums[32];
   __shared__ TreeMaskBuf masks;
@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
     const bool good = pc.good;
     __syncthreads();
     if (threadIdx.x < 32) tree_masks(g, a, b, good, &masks);
-    const int nr = min(kTile, g.G * g.T - r0);
-    for (int i = threadIdx.x; i < kTile * (D / 8); i += kThreads) {
+    const int nr = min(ROWS, g.G * g.T - r0);
+    for (int i = threadIdx.x; i < ROWS * (D / 8); i += 4 * ROWS) {
       const int r = i / (D / 8), c = i - r * (D / 8), ra = r0 + r;
       const T* src = r < nr ? view_at<T>(a.q, b, hk * g.G + ra / g.T, ra % g.T) + c * 8 : nullptr;
 #pragma unroll
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
         return good && (u < 0 || (u < g.T && ((used >> u) & 1)));
       };
       __syncthreads();
-      load_rows_if<T, D>(Ks, D + 4, view_at<T>(a.k, b, hk, k0), a.k.row, wanted);
-      load_rows_if<T, D>(Vs, D, view_at<T>(a.v, b, hk, k0), a.v.row, wanted);
+      load_rows_if<T, D, kTile>(Ks, D + 4, view_at<T>(a.k, b, hk, k0), a.k.row, wanted);
+      load_rows_if<T, D, kTile>(Vs, D, view_at<T>(a.v, b, hk, k0), a.v.row, wanted);
       __syncthreads();
       float s[4][4];
       mul_nt<D>(s, Qs, D + 4, Ks, D + 4);
@@ -97,20 +97,21 @@ __global__ void __launch_bounds__(kThreads, 2) tree_simt_kernel(TreeGeo g, TreeA
   }
 }
 
-template <typename T, int D>
+template <int D, int ROWS>
 cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
-  auto kern = tree_simt_kernel<T, D>;
-  const int smem = tree_smem<D>() + (g.B + 1) * 4;
+  auto kern = tree_simt_kernel<float, D, ROWS>;
+  const int smem = tree_smem<D, ROWS>() + (g.B + 1) * 4;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<g.C, kThreads, smem, st>>>(g, a);
+  kern<<<g.C, 4 * ROWS, smem, st>>>(g, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tree_simt(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
-  return g.d == 64 ? launch<float, 64>(g, a, st) : launch<float, 128>(g, a, st);
+  if (g.RR == 32) return g.d == 64 ? launch<64, 32>(g, a, st) : launch<128, 32>(g, a, st);
+  return g.d == 64 ? launch<64, 64>(g, a, st) : launch<128, 64>(g, a, st);
 }
 
 }  // namespace pyr

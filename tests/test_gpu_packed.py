@@ -6,6 +6,15 @@ element for the gradients. bf16: the inputs are exact; P (forward), P and dS (ba
 once (2^-8 relative each, averaging over the keys), and the outputs are rounded once (2^-8): max-abs error
 <= 2^-8 |x| + 2^-7 max over the row's keys of |v| for O; for the gradients relative L2 <= 3 * 2^-8 and
 max-abs <= 2^-5 of the largest element; D comes from a bf16 O.
+
+Where dP and D cancel (a row that sees one key has dP = D and a gradient of zero) the error does not scale
+with the gradient but with the cancelled terms. dP is a sum of d products in two fp32 chains of d/2: each term
+is rounded at most d/2 + 1 times, so |error of dP| <= g A with g = (d/2 + 2) 2^-24 and A = sum |dO||v| over
+the row's elements (bf16: the products are exact in fp32, the same bound holds); D has the same bound with
+O, |O| <= max |v|. P sums to one over a row, so |error of dQ| <= 2 g A max|k| / sqrt(d), and dK the same with
+max|q| and the number of rows that see the key, whose P do not sum to one: each P <= 1. That term is added to
+the bounds above (for dK with one row, where it matters; elsewhere the relative bound is the larger one). In
+bf16, D is taken from a rounded O: |error of D| <= 2^-9 A more.
 """
 import pytest
 import torch
@@ -111,11 +120,15 @@ def test_backward_against_the_formula(case):
     want = ref.packed_grad(Q[:, sl], K[:, sl], V[:, sl], dO[:, sl], [c - a for c in cu])
     for got, w, name in zip((dQ, dK, dV), want, ("dQ", "dK", "dV")):
         e = (got[:, sl].double() - w).abs()
-        top = max(float(w.abs().max()), 1e-3)
+        top = float(w.abs().max())
+        A = float(dO[:, sl].abs().double().sum(-1).max() * V[:, sl].abs().double().max())
+        A = min(A, float(dO[:, sl].double().norm(dim=-1).max() * V[:, sl].double().norm(dim=-1).max()))
+        g = (d / 2 + 2) * 2.0 ** -24 + (2.0 ** -9 / 2 if dtype == BF16 else 0)
+        cancelled = 0.0 if name == "dV" else 2 * g * A * float((K if name == "dQ" else Q)[:, sl].abs().max()) / d ** 0.5
         if dtype == F32:
-            assert float(e.max()) <= 1e-4 * top, (name, float(e.max()), top)
+            assert float(e.max()) <= 1e-4 * top + cancelled, (name, float(e.max()), top, cancelled)
         else:
-            assert float(e.max()) <= 2.0 ** -5 * top, (name, float(e.max()), top)
+            assert float(e.max()) <= 2.0 ** -5 * top + cancelled, (name, float(e.max()), top, cancelled)
             if float(w.norm()) > 1e-2:
                 assert float(e.norm() / w.norm()) <= 3 * 2.0 ** -8, (name, float(e.norm() / w.norm()))
     # the same call again gives the same bits
