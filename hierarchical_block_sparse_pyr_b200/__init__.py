@@ -147,7 +147,7 @@ def _load_lib():
     lib.phba_state_build.restype = ctypes.c_int
     lib.phba_forward.argtypes = [sp, vp, vp, vp, vp, vp, ctypes.c_int, vp, vp, vp, vp, vp, vp]
     lib.phba_forward.restype = ctypes.c_int
-    vw, ps, ts = ctypes.POINTER(PyrView), ctypes.POINTER(PackedShape), ctypes.POINTER(TreeShape)
+    vw, ps, ts = vp, ctypes.POINTER(PackedShape), ctypes.POINTER(TreeShape)  # (vw: a PyrView's address)
     i, dbl = ctypes.c_int, ctypes.c_double
     lib.rope_spec_init.argtypes = [ctypes.POINTER(RopeSpec), i, i, i, dbl, i, dbl, i]
     lib.rope_apply.argtypes = [ctypes.POINTER(RopeSpec), i, i, i, i, i, vw, vw, vp, ctypes.c_int64, i, vw, vw, i, vp,
@@ -392,20 +392,43 @@ def _dtype_code(dtype):
     return int(dtype)
 
 
-def _view(t, name, shape, dtype, device):
-    """PyrView of a tensor [batch, head, row, d] or [head, row, d] of any strides with adjacent elements."""
+_TORCH_DTYPES = {v: k for k, v in _DTYPES.items()}
+_VIEW_ARRAYS = {n: ctypes.c_int64 * (4 * n) for n in range(1, 9)}
+
+
+def _refuse(t, name, shape, dtype, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if _DTYPES.get(t.dtype) != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, which is not the call's")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, the call's is {dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on another device than the other operands")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"the elements of a row of {name} must be adjacent")
-    return PyrView(t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    raise ValueError(f"the elements of a row of {name} must be adjacent")
+
+
+def _views(dtype, device, operands):
+    """pyr_views of (tensor, name, shape) operands, tensors [batch, head, row, d] or [head, row, d] of any
+    strides with adjacent elements: the array that holds them and their addresses."""
+    td = _TORCH_DTYPES.get(dtype)
+    vals = []
+    for t, name, shape in operands:
+        if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not td or t.get_device() != device or \
+                device < 0:
+            _refuse(t, name, shape, td, device)
+        st = t.stride()
+        if st[-1] != 1:
+            _refuse(t, name, shape, td, device)
+        vals += (t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    n = len(vals) // 4
+    arr = _VIEW_ARRAYS[n](*vals)
+    base = ctypes.addressof(arr)
+    return arr, [base + 32 * i for i in range(n)]
+
+
+def _device_of(t):
+    return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
 def _plain(t, name, dtype, numel, device, nullable=False):
@@ -414,7 +437,7 @@ def _plain(t, name, dtype, numel, device, nullable=False):
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on another device than the other operands")
@@ -428,9 +451,10 @@ def _call(fn, what, device, stream, *args):
     if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
             return _call(fn, what, device, stream, *args)
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    _check(fn(*args, _stream(stream)), what)
+    raw = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+    rc = fn(*args, raw)
+    if rc:
+        raise PyrError(rc, what)
 
 
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -465,23 +489,24 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
     if d != spec.d:
         raise ValueError(f"the spec is for d = {spec.d}, not {d}")
     dt, dev = _dtype_code(first.dtype), first.get_device()
-    views, heads = [None] * 4, [0, 0]
+    operands, heads = [], [0, 0]
     for i, (x, y, name) in enumerate(((Q, Qo, "Q"), (K, Ko, "K"))):
         if x is None:
             continue
-        if x.dim() != 4 or x.shape[1] < 1:
+        if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[1] < 1:
             raise ValueError(f"{name} must be [B, H, N, d]")
         heads[i] = x.shape[1]
         shape = (B, heads[i], N, d)
-        views[i] = _view(x, name, shape, dt, dev)
-        views[2 + i] = _view(y, name + "o", shape, dt, dev)
+        operands += ((x, name, shape), (y, name + "o", shape))
+    arr, v = _views(dt, dev, operands)
+    q, qo = (v[0], v[1]) if Q is not None else (None, None)
+    k, ko = (v[-2], v[-1]) if K is not None else (None, None)
     stride = 0
+    p = _plain(pos, "pos", torch.int32, 0, dev, True)
     if pos is not None:
-        if tuple(pos.shape) not in ((N,), (B, N)):
+        if pos.shape != (B, N) and pos.shape != (N,):
             raise ValueError("pos must be [B, N] or [N]")
         stride = N if pos.dim() == 2 else 0
-    p = _plain(pos, "pos", torch.int32, 0, dev, True)
-    q, k, qo, ko = (None if v is None else ctypes.byref(v) for v in views)
     _call(_L().rope_apply, "rope_apply", dev, stream, ctypes.byref(spec), B, heads[0], heads[1], N, dt, q, k, p, stride,
           int(pos_offset), qo, ko, int(bool(inverse)), _plain(status, "status", torch.int32, 1, dev, True))
 
@@ -498,7 +523,7 @@ def packed_plan_elems(s: PackedShape) -> int:
 def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
     """The work list of sequences [cu[i], cu[i+1]) (int32 CUDA tensor [S + 1]); it serves every packed_forward
     and packed_backward of this shape and these boundaries. Returns plan (allocated if None)."""
-    dev = cu.get_device() if isinstance(cu, torch.Tensor) else -1
+    dev = _device_of(cu)
     c = _plain(cu, "cu", torch.int32, s.S + 1, dev)
     n = packed_plan_elems(s)
     if plan is None:
@@ -511,11 +536,11 @@ def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
 def packed_forward(s: PackedShape, Q, K, V, plan, O, lse=None, status=None, stream=None):
     """Causal attention inside every packed sequence: Q, O [Hq, T, d], K, V [Hkv, T, d] (any strides), lse fp32
     [Hq, T]. Tokens outside the sequences are neither used nor written."""
-    dev = Q.get_device() if isinstance(Q, torch.Tensor) else -1
-    q, kv, dt = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d), s.dtype
-    v = [_view(Q, "Q", q, dt, dev), _view(K, "K", kv, dt, dev), _view(V, "V", kv, dt, dev), _view(O, "O", q, dt, dev)]
-    _call(_L().packed_forward, "packed_forward", dev, stream, ctypes.byref(s), *map(ctypes.byref, v[:3]),
-          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), ctypes.byref(v[3]),
+    dev = _device_of(Q)
+    q, kv = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d)
+    arr, v = _views(s.dtype, dev, ((Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q)))
+    _call(_L().packed_forward, "packed_forward", dev, stream, ctypes.byref(s), v[0], v[1], v[2],
+          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), v[3],
           _plain(lse, "lse", torch.float32, s.Hq * s.T, dev, True),
           _plain(status, "status", torch.int32, 1, dev, True))
 
@@ -523,15 +548,14 @@ def packed_forward(s: PackedShape, Q, K, V, plan, O, lse=None, status=None, stre
 def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV, status=None, stream=None):
     """Gradients of packed_forward for dO, from its O and lse: dQ, dK, dV (views like Q, K, V), with delta an
     fp32 workspace [Hq, T]."""
-    dev = Q.get_device() if isinstance(Q, torch.Tensor) else -1
-    q, kv, dt = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d), s.dtype
-    v = {n: _view(t, n, sh, dt, dev) for n, t, sh in (("Q", Q, q), ("K", K, kv), ("V", V, kv), ("O", O, q),
-                                                      ("dO", dO, q), ("dQ", dQ, q), ("dK", dK, kv), ("dV", dV, kv))}
-    r = {n: ctypes.byref(x) for n, x in v.items()}
-    _call(_L().packed_backward, "packed_backward", dev, stream, ctypes.byref(s), r["Q"], r["K"], r["V"],
-          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), r["O"],
-          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev), r["dO"],
-          _plain(delta, "delta", torch.float32, s.Hq * s.T, dev), r["dQ"], r["dK"], r["dV"],
+    dev = _device_of(Q)
+    q, kv = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d)
+    arr, v = _views(s.dtype, dev, ((Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q), (dO, "dO", q), (dQ, "dQ", q),
+                                   (dK, "dK", kv), (dV, "dV", kv)))
+    _call(_L().packed_backward, "packed_backward", dev, stream, ctypes.byref(s), v[0], v[1], v[2],
+          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), v[3],
+          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev), v[4],
+          _plain(delta, "delta", torch.float32, s.Hq * s.T, dev), v[5], v[6], v[7],
           _plain(status, "status", torch.int32, 1, dev, True))
 
 
@@ -548,13 +572,13 @@ def tree_forward(s: TreeShape, Q, K, V, lens, parent, O, lse=None, workspace=Non
     """Attention of drafted tokens: Q, O [B, Hq, T, d], caches K, V [B, Hkv, N, d] (any strides), lens int32 [B]
     context lengths, parent int32 [B, T] (None: a chain), lse fp32 [B, Hq, T]; the drafted tokens' keys and
     values are in the cache rows lens[b] + t. workspace: a CUDA uint8 tensor of tree_workspace_bytes(s) bytes."""
-    dev = Q.get_device() if isinstance(Q, torch.Tensor) else -1
-    q, kv, dt = (s.B, s.Hq, s.T, s.d), (s.B, s.Hkv, s.N, s.d), s.dtype
-    v = [_view(Q, "Q", q, dt, dev), _view(K, "K", kv, dt, dev), _view(V, "V", kv, dt, dev), _view(O, "O", q, dt, dev)]
+    dev = _device_of(Q)
+    q, kv = (s.B, s.Hq, s.T, s.d), (s.B, s.Hkv, s.N, s.d)
+    arr, v = _views(s.dtype, dev, ((Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q)))
     w = _plain(workspace, "workspace", torch.uint8, 0, dev)
-    _call(_L().tree_forward, "tree_forward", dev, stream, ctypes.byref(s), *map(ctypes.byref, v[:3]),
-          _plain(lens, "lens", torch.int32, s.B, dev), _plain(parent, "parent", torch.int32, s.B * s.T, dev, True),
-          ctypes.byref(v[3]), _plain(lse, "lse", torch.float32, s.B * s.Hq * s.T, dev, True), w, workspace.numel(),
+    _call(_L().tree_forward, "tree_forward", dev, stream, ctypes.byref(s), v[0], v[1], v[2],
+          _plain(lens, "lens", torch.int32, s.B, dev), _plain(parent, "parent", torch.int32, s.B * s.T, dev, True), v[3],
+          _plain(lse, "lse", torch.float32, s.B * s.Hq * s.T, dev, True), w, workspace.numel(),
           _plain(status, "status", torch.int32, 1, dev, True))
 
 

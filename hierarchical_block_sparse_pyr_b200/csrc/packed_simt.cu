@@ -72,23 +72,38 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
   }
 }
 
-// delta[t] = dO_t . O_t for the rows of the sequences; one warp a row
+// delta[t] = dO_t . O_t for the rows of the sequences. A row is read by as many lanes as it has 16-byte
+// chunks, and a thread has four rows' chunks of both tensors in flight: one pass, bound by HBM.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) packed_delta_kernel(PackedGeo g, PackedBwdArgs a) {
+  constexpr int E = 16 / sizeof(T), L = D / E, U = 4;  // elements a chunk, lanes a row, rows a thread
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
   if (tile >= a.plan[kListQ]) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x % L;
   const int stop = min(w.z + packed_tile_rows(g, kListQ), w.y);
-  constexpr int E = D / 32;
-  for (int t = w.z + (threadIdx.x >> 5); t < stop; t += 8) {
-    const T *o = view_at<T>(a.o, 0, h, t) + lane * E, *d = view_at<T>(a.dout, 0, h, t) + lane * E;
-    float s = 0.f;
+  for (int t0 = w.z + threadIdx.x / L; t0 < stop; t0 += U * (256 / L)) {
+    uint4 o[U], d[U];
 #pragma unroll
-    for (int e = 0; e < E; e++) s = fmaf(to_f32(o[e]), to_f32(d[e]), s);
+    for (int u = 0; u < U; u++) {
+      const int t = t0 + u * (256 / L);
+      o[u] = d[u] = make_uint4(0, 0, 0, 0);
+      if (t < stop) {
+        o[u] = __ldcs(reinterpret_cast<const uint4*>(view_at<T>(a.o, 0, h, t)) + lane);
+        d[u] = __ldg(reinterpret_cast<const uint4*>(view_at<T>(a.dout, 0, h, t)) + lane);
+      }
+    }
 #pragma unroll
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (lane == 0) a.delta[(int64_t)h * g.T + t] = s;
+    for (int u = 0; u < U; u++) {
+      const T *x = reinterpret_cast<const T*>(&o[u]), *y = reinterpret_cast<const T*>(&d[u]);
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; e++) s = fmaf(to_f32(x[e]), to_f32(y[e]), s);
+#pragma unroll
+      for (int m = L / 2; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      const int t = t0 + u * (256 / L);
+      if (lane == 0 && t < stop) a.delta[(int64_t)h * g.T + t] = s;
+    }
   }
 }
 

@@ -83,17 +83,7 @@ cudaError_t launch_join(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
   const int rows = used < g.RR ? used : g.RR;
   const dim3 grid(g.B * g.Hkv * g.RG, (rows + kJoinWarps - 1) / kJoinWarps);
   // launched while the kernel before it still runs; it works out its segments and then waits for the parts
-  cudaLaunchAttribute early = {};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = (g.B + 1) * sizeof(int);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_join_kernel<T, D>, g, a);
+  return launch_early(tree_join_kernel<T, D>, grid, dim3(kJoinWarps * 32), (g.B + 1) * sizeof(int), st, g, a);
 }
 
 int make_tree_geo(const tree_shape* s, TreeGeo* g) {

@@ -5,11 +5,6 @@
 
 namespace pyr {
 
-// Overlap of two kernels of a stream: the second may start once every block of the first has called
-// grid_launch (or has ended), and waits in grid_wait until the first has ended and its writes are visible.
-__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Rows of a unit (sequence, key/value head): drafted token t of the group's head h. They are cut into row
 // groups of RR rows, and the keys into tiles of BK. On the CUDA cores (HM = 0) row r = h * T + t is row
 // r % RR of group r / RR; on the tensor cores a group is RR / 128 tiles that hold the T rows of HM heads each.

@@ -15,6 +15,27 @@ __device__ __forceinline__ T* view_at(const View& v, int b, int h, int64_t n) {
   return reinterpret_cast<T*>(v.data) + (b * v.batch + h * v.head + n * v.row);
 }
 
+// Overlap of two kernels of a stream: the second may start once every block of the first has called
+// grid_launch (or has ended), and waits in grid_wait until the first has ended and its writes are visible.
+__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch a kernel that may start early in this sense.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 inline int elt_bytes(int dtype) { return dtype == PYR_F32 ? 4 : 2; }
