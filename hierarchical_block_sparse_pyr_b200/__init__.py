@@ -528,6 +528,8 @@ def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
     n = packed_plan_elems(s)
     if plan is None:
         plan = torch.empty(max(n, 1), dtype=torch.int32, device=cu.device)
+        if isinstance(stream, torch.cuda.Stream):
+            plan.record_stream(stream)
     _call(_L().packed_plan, "packed_plan", dev, stream, ctypes.byref(s), c,
           _plain(plan, "plan", torch.int32, n, dev), _plain(status, "status", torch.int32, 1, dev, True))
     return plan

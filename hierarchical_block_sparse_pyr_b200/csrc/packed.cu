@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedGeo g, 
   __shared__ int s_bad, s_most;
   const int tid = threadIdx.x;
   if (tid == 0) s_bad = 0;
-  if (tid < kPlanHeader) plan[tid] = 0;
+  if (tid < kPlanHeader) plan[tid] = tid == 3 ? packed_plan_mark(g) : 0;
   __syncthreads();
   for (int s = tid; s < g.S; s += kPlanThreads) {
     const int a = cu[s], b = cu[s + 1];

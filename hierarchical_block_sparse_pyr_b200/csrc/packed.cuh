@@ -10,7 +10,8 @@ struct PackedGeo {
 };
 
 // A plan is three work lists, each sorted by work (longest first), behind a header of kPlanHeader int32
-// words of which the first three are the lists' lengths:
+// words of which the first three are the lists' lengths and the fourth marks the geometry they are for
+// (entries of another shape, or a buffer that holds no plan, would send the kernels out of bounds):
 //   kListFwd   row tiles of the forward pass,   work ~ keys up to the tile's end
 //   kListQ     row tiles of the dQ kernel,      same
 //   kListK     key tiles of the dK/dV kernel,   work ~ rows from the tile's start to the sequence's end
@@ -37,6 +38,23 @@ __host__ __device__ inline int64_t packed_list_at(const PackedGeo& g, int list) 
   return at;
 }
 __host__ __device__ inline int64_t packed_plan_words(const PackedGeo& g) { return packed_list_at(g, 3) + g.S + 1; }
+
+__host__ __device__ inline int packed_plan_mark(const PackedGeo& g) {
+  const uint32_t v[7] = {(uint32_t)g.S, (uint32_t)g.T, (uint32_t)g.Hq, (uint32_t)g.Hkv, (uint32_t)g.d, (uint32_t)g.dtype,
+                         0x706c616eu};
+  uint32_t h = 2166136261u;  // FNV-1a over the words
+  for (int i = 0; i < 7; i++) h = (h ^ v[i]) * 16777619u;
+  return (int)(h | 1u);
+}
+
+// Length of a list, 0 where the plan is not one of this geometry (reported once by the grid).
+__device__ __forceinline__ int packed_tiles(const PackedGeo& g, const int32_t* plan, int list, int* status) {
+  if (plan[3] != packed_plan_mark(g)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) report(status, PYR_EBADSEQ);
+    return 0;
+  }
+  return plan[list];
+}
 
 struct PackedFwdArgs {
   View q, k, v, o;

@@ -103,9 +103,9 @@ struct KItem {
   int end, key0, hk, nq, steps;
 };
 
-__device__ __forceinline__ bool k_item(const PackedGeo& g, const int32_t* plan, int64_t at, KItem* it) {
+__device__ __forceinline__ bool k_item(const PackedGeo& g, const int32_t* plan, int tiles, int64_t at, KItem* it) {
   const int64_t tile = at / g.Hkv;
-  if (tile >= uniform(plan[kListK])) return false;
+  if (tile >= tiles) return false;
   const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListK)) + tile);
   it->hk = (int)(at - tile * g.Hkv);
   it->end = uniform(w.y);
@@ -182,13 +182,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS = tmem, tP = tmem + 128, tDV = tmem + 256, tDK = tmem + 256 + D;
   const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024), dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
   KItem it;
+  const int tiles = uniform(packed_tiles(g, a.plan, kListK, a.status));
 
   if (warp == kSoftmax + 0) {
     regs_dec<64>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int items = 0, u = 0;
-    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && k_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       if (items > 0) ok = warp_wait(bar_kv_free, (items - 1) & 1, abort_flag);
       if (!ok) break;
       if (elect_one()) {
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dGm = sdesc_sw128(smem_u32(smem + PL::kG), 16384, 1024);
     bool ok = true;
     int items = 0, u = 0;
-    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && k_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       int j = 0;  // query tile that the next S reads
       auto scores = [&](int v) {
         const int s = v % NS;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ lse, delta, tails
     bool ok = true;
     int u = 0;
-    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++) {
+    for (int r = 0; ok && k_item(g, a.plan, tiles, list_at(r), &it); r++) {
       for (int i = 0; i < it.steps; i++, u++) {
         const int s = u % NS, k = u / NS, head = it.hk * g.G + i / it.nq, q0 = it.key0 + i % it.nq * 128;
         if (k > 0) ok = warp_wait(bar_st_free + s, (k - 1) & 1, abort_flag);
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rr = wq * 32 + lane;
     bool ok = true;
     int items = 0, u = 0;
-    for (int r = 0; ok && k_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && k_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       const bool live = it.key0 + wq * 32 < it.end;
       int j = 0;
       for (int i = 0; i < it.steps; i++, u++) {
@@ -452,9 +453,9 @@ struct QItem {
   int start, end, row0, head, hk, steps;
 };
 
-__device__ __forceinline__ bool q_item(const PackedGeo& g, const int32_t* plan, int64_t at, QItem* it) {
+__device__ __forceinline__ bool q_item(const PackedGeo& g, const int32_t* plan, int tiles, int64_t at, QItem* it) {
   const int64_t tile = at / g.Hq;
-  if (tile >= uniform(plan[kListQ])) return false;
+  if (tile >= tiles) return false;
   const int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListQ)) + tile);
   it->head = (int)(at - tile * g.Hq);
   it->hk = it->head / g.G;
@@ -530,13 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tS = tmem, tP = tmem + 256, tDQ = tmem + 384;  // S[b] at 128 b
   const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024);
   QItem it;
+  const int tiles = uniform(packed_tiles(g, a.plan, kListQ, a.status));
 
   if (warp == kSoftmax + 0) {
     regs_dec<64>();
     // ------------------------------------------------------------ TMA producer
     bool ok = true;
     int items = 0, u = 0;
-    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       if (items > 0) ok = warp_wait(bar_q_free, (items - 1) & 1, abort_flag);
       if (!ok) break;
       if (elect_one()) {
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int us = 0, si = 0, sr = 0, sitems = 0;  // next S: step, step of its item, item
     QItem is;
-    bool more = q_item(g, a.plan, list_at(0), &is);
+    bool more = q_item(g, a.plan, tiles, list_at(0), &is);
     auto scores = [&]() {
       if (!more || !ok) return;
       const int s = us % NK, b = us & 1;
@@ -597,13 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++si == is.steps) {
         si = 0;
         sitems++;
-        more = q_item(g, a.plan, list_at(++sr), &is);
+        more = q_item(g, a.plan, tiles, list_at(++sr), &is);
       }
     };
     scores();
     scores();
     int items = 0, u = 0;
-    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       for (int i = 0; i < it.steps && ok; i++, u++) {
         const int b = u & 1, s = u % NK;
         ok = warp_wait(bar_ds_full + b, (u >> 1) & 1, abort_flag);
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
     bool ok = true;
     int items = 0, u = 0;
-    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       ok = warp_wait(bar_q_full, items & 1, abort_flag);
       for (int i = 0; i < it.steps && ok; i++, u++) {
         const int s = u % NV;
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rr = wq * 32 + lane;
     bool ok = true;
     int items = 0, u = 0;
-    for (int r = 0; ok && q_item(g, a.plan, list_at(r), &it); r++, items++) {
+    for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       const int row = it.row0 + rr;
       const bool live = it.row0 + wq * 32 < it.end;
       const int64_t at = (int64_t)it.head * g.T + min(row, it.end - 1);

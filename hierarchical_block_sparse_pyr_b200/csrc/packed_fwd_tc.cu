@@ -49,11 +49,11 @@ struct FItem {
   int steps;
 };
 
-__device__ __forceinline__ bool fwd_item(const PackedGeo& g, const int32_t* plan, int64_t at, FItem* it) {
+__device__ __forceinline__ bool fwd_item(const PackedGeo& g, const int32_t* plan, int tiles, int64_t at, FItem* it) {
   const bool pair = g.G % 2 == 0;
   const int units = pair ? g.Hq / 2 : g.Hq;
   const int64_t tile = at / units;
-  if (tile >= uniform(plan[kListFwd])) return false;
+  if (tile >= tiles) return false;
   const int u = (int)(at - tile * units);
   int4 w = __ldg(reinterpret_cast<const int4*>(plan + packed_list_at(g, kListFwd)) + tile);
   w.x = it->start = uniform(w.x);
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
   unsigned char* ring = smem + PL::kRing;
 
   FItem it;
+  const int tiles = uniform(packed_tiles(g, a.plan, kListFwd, a.status));
   // a softmax thread holds a row of 128 scores; the other warpgroup needs few registers
   // (2 * 128 * 208 + 128 * 88 = 384 * 168)
   if (warp == 8) {
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     bool ok = true;
     int u = 0;  // ring uses so far
     int nq[2] = {0, 0};
-    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
+    for (int r = 0; ok && fwd_item(g, a.plan, tiles, list_at(r), &it); r++) {
       auto load = [&](const CUtensorMap* map, int row) {
         const int s = u % NS, k = u / NS;
         if (k > 0 && ok) ok = warp_wait(bar_free + s, (k - 1) & 1, abort_flag);
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dK = sdesc_sw128(smem_u32(ring), 16, 1024);
     bool ok = true;
     int u = 0, nq[2] = {0, 0}, ns[2] = {0, 0};
-    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
+    for (int r = 0; ok && fwd_item(g, a.plan, tiles, list_at(r), &it); r++) {
       for (int t = 0; t < it.steps; t++, u += 2) {
         const int s = u % NS;
         ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     const uint64_t dV = sdesc_sw128(smem_u32(ring), 16384, 1024);
     bool ok = true;
     int u = 1, np[2] = {0, 0}, no[2] = {0, 0};
-    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
+    for (int r = 0; ok && fwd_item(g, a.plan, tiles, list_at(r), &it); r++) {
       for (int t = 0; t < it.steps && ok; t++, u += 2) {
         const int s = u % NS;
         ok = warp_wait(bar_full + s, (u / NS) & 1, abort_flag);
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
     const float sl2 = rsqrtf((float)D) * kLog2e;
     bool ok = true;
     int n = 0, turns = 0;  // so far: tiles of S, turns of the other row tile waited for
-    for (int r = 0; ok && fwd_item(g, a.plan, list_at(r), &it); r++) {
+    for (int r = 0; ok && fwd_item(g, a.plan, tiles, list_at(r), &it); r++) {
       const int steps = mt ? it.n[1] : it.n[0], row_mt = mt ? it.row[1] : it.row[0];
       const int head = mt ? it.head[1] : it.head[0];
       if (!steps) continue;

@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm, *Ks = Qs + kRows * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
-  if (tile >= a.plan[kListFwd]) return;
+  if (tile >= packed_tiles(g, a.plan, kListFwd, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListFwd))[tile];
   const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -78,7 +78,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) packed_delta_kernel(PackedGeo g, PackedBwdArgs a) {
   constexpr int E = 16 / sizeof(T), L = D / E, U = 4;  // elements a chunk, lanes a row, rows a thread
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
-  if (tile >= a.plan[kListQ]) return;
+  if (tile >= packed_tiles(g, a.plan, kListQ, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
   const int lane = threadIdx.x % L;
   const int stop = min(w.z + packed_tile_rows(g, kListQ), w.y);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
   constexpr int P = D + 4;
   float *Qs = sm, *Gs = Qs + kRows * P, *Ks = Gs + kRows * P, *Vs = Ks + kTile * P, *Ps = Vs + kTile * P;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
-  if (tile >= a.plan[kListQ]) return;
+  if (tile >= packed_tiles(g, a.plan, kListQ, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
   const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g,
   constexpr int P = D + 4;
   float *Ks = sm, *Vs = Ks + kRows * P, *Qs = Vs + kRows * P, *Gs = Qs + kTile * P, *Ps = Gs + kTile * P;
   const int tile = blockIdx.x / g.Hkv, hk = blockIdx.x - tile * g.Hkv;
-  if (tile >= a.plan[kListK]) return;
+  if (tile >= packed_tiles(g, a.plan, kListK, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListK))[tile];
   const int end = w.y, key0 = w.z;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;

@@ -175,12 +175,13 @@ void launch_vec(const RopeArgs& a, cudaStream_t st) {
 
 template <typename T, int LAYOUT>
 void launch_layout(const RopeArgs& a, cudaStream_t st) {
-  // few tokens: one head a thread, so that the heads spread over the GPU; else eight share their angles
+  // few tokens: one head a thread, so that the heads spread over the GPU; else four share their angles (32K
+  // tokens, 32 heads of 128, bf16: 81.8 us; two 100.5, eight 83.4)
   const int64_t threads = (int64_t)a.B * a.N * (a.Hq + a.Hkv) * a.d / (2 * Vec<T>::E);
   if (threads <= 148 * 2048)
     launch_vec<T, LAYOUT, 1>(a, st);
   else
-    launch_vec<T, LAYOUT, 8>(a, st);
+    launch_vec<T, LAYOUT, 4>(a, st);
 }
 
 template <typename T>

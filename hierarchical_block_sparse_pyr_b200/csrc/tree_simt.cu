@@ -83,6 +83,12 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
     for (int i = 0; i < 4; i++) {
       const int r = 4 * ty + i;
       if (r >= nr) continue;
+      if (mask[i] == 0) {  // an absent slot: what it summed is not its own
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
+      }
       if (whole) {
         const int h = hk * g.G + (r0 + r) / g.T, t = (r0 + r) % g.T;
         store_row<T, D>(view_at<T>(a.o, b, h, t), acc[i], l[i] > 0.f ? 1.f / l[i] : 0.f);

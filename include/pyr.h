@@ -547,7 +547,9 @@ PYR_API int packed_plan(const packed_shape* s, const int32_t* cu, int32_t* plan,
 /*
  * packed_forward - causal attention of every sequence of the batch.
  *   Q, O   views [Hq][T][d]; K, V views [Hkv][T][d] (batch strides ignored).
- *   plan   device, as written by packed_plan for the same shape.
+ *   plan   device, as written by packed_plan for the same shape. A buffer that
+ *          is not a plan of this shape gives no work, and PYR_EBADSEQ is
+ *          reported in *dev_status.
  *   lse    device fp32 [Hq][T] or NULL (written): natural log-sum-exp.
  * bf16 runs on the tcgen05 tensor cores with fp32 statistics and accumulators
  * (probabilities are rounded to bf16 for the second product); fp32 runs in

@@ -210,3 +210,109 @@ def test_packed_under_a_graph():
     assert torch.equal(O, O2) and torch.equal(lse, lse2)
     for x, y in zip(grads, g2):
         assert torch.equal(x, y)
+
+
+def test_a_plan_of_another_shape_does_nothing_but_report():
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    cu, T, Q, K, V, dO = _batch([100, 28], 0, 2, 2, 64, BF16, "hnd", 61)
+    s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+    other = P.packed_shape(2, T, 2, 2, 64, F32)
+    foreign = torch.zeros(max(P.packed_plan_elems(s), P.packed_plan_elems(other)), dtype=torch.int32, device="cuda")
+    cut = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    for buf in (P.packed_plan(other, cut, foreign), torch.full_like(foreign, 2 ** 31 - 1)):
+        for call in ("forward", "backward"):
+            out = [torch.full_like(x, 3.0) for x in (Q, Q, K, V)]
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            if call == "forward":
+                P.packed_forward(s, Q, K, V, buf, out[0], status=status)
+            else:
+                P.packed_backward(s, Q, K, V, buf, O, lse, dO, torch.empty_like(lse), *out[1:], status=status)
+            torch.cuda.synchronize()
+            assert int(status) == P.PYR_EBADSEQ and all((x == 3).all() for x in out)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_views_into_larger_tensors(dtype, d):
+    """Q, K and V as slices of one projection [T, Hq + 2 Hkv, d] with a padded row, outputs in another layout."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    Hq, Hkv, lens = 6, 3, [200, 1, 77]
+    T = sum(lens)
+    g = torch.Generator().manual_seed(71)
+    wide = torch.randn((T, Hq + 2 * Hkv, d + 8), generator=g).to(dtype).cuda()
+    x = wide[..., 8:].transpose(0, 1)  # rows start 16 or 32 bytes into their pitch
+    Q, K, V = x[:Hq], x[Hq:Hq + Hkv], x[Hq + Hkv:]
+    cu = [0, 200, 201, 278]
+    s = P.packed_shape(3, T, Hq, Hkv, d, dtype)
+    plan = P.packed_plan(s, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    O = torch.empty((Hq, T, d), dtype=dtype, device="cuda")
+    lse = torch.empty((Hq, T), device="cuda")
+    P.packed_forward(s, Q, K, V, plan, O, lse)
+    O2 = torch.empty((T, Hq, d), dtype=dtype, device="cuda").transpose(0, 1)
+    P.packed_forward(s, Q.contiguous(), K.contiguous(), V.contiguous(), plan, O2)
+    assert torch.equal(O, O2)
+    wo, _ = ref.packed(Q, K, V, cu)
+    assert float((O.double() - wo).abs().max()) <= (2e-5 if dtype == F32 else 2.0 ** -7) * float(V.abs().max()) * 2
+    dO = torch.randn((T, Hq, d), generator=g).to(dtype).cuda().transpose(0, 1)
+    grad = torch.zeros_like(wide)  # the gradient of the projection, written through the same slices
+    gx = grad[..., 8:].transpose(0, 1)
+    P.packed_backward(s, Q, K, V, plan, O, lse, dO, torch.empty_like(lse), gx[:Hq], gx[Hq:Hq + Hkv], gx[Hq + Hkv:])
+    plain = [torch.empty_like(t) for t in (O, K.contiguous(), V.contiguous())]
+    P.packed_backward(s, Q.contiguous(), K.contiguous(), V.contiguous(), plan, O, lse, dO.contiguous(),
+                      torch.empty_like(lse), *plain)
+    assert torch.equal(gx[:Hq], plain[0]) and torch.equal(gx[Hq:Hq + Hkv], plain[1])
+    assert torch.equal(gx[Hq + Hkv:], plain[2]) and (grad[..., :8] == 0).all()
+
+
+def test_two_batches_on_two_streams():
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    jobs = []
+    for seed, lens in ((81, [700, 40, 1300]), (82, [1025, 3, 511])):
+        cu, T, Q, K, V, dO = _batch(lens, 0, 8, 2, 128, BF16, "nhd", seed)
+        s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+        want = [torch.empty_like(x) for x in (Q, K, V)]
+        P.packed_backward(s, Q, K, V, plan, O, lse, dO, torch.empty_like(lse), *want)
+        jobs.append((torch.cuda.Stream(), s, plan, (Q, K, V), dO, O, lse, want))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for st, s, plan, x, dO, O, lse, want in jobs:
+            o, z, dl = torch.zeros_like(O), torch.zeros_like(lse), torch.zeros_like(lse)
+            gr = [torch.zeros_like(t) for t in x]
+            got.append((o, z, gr, dl))
+        torch.cuda.synchronize()
+        for (st, s, plan, x, dO, O, lse, want), (o, z, gr, dl) in zip(jobs, got):
+            P.packed_forward(s, *x, plan, o, z, stream=st)
+            P.packed_backward(s, *x, plan, o, z, dO, dl, *gr, stream=st)
+        torch.cuda.synchronize()
+        for (st, s, plan, x, dO, O, lse, want), (o, z, gr, dl) in zip(jobs, got):
+            assert torch.equal(o, O) and torch.equal(z, lse) and all(torch.equal(a, b) for a, b in zip(gr, want))
+
+
+def test_rotate_attend_and_train_in_one_stream():
+    """The operators as they are used: rotate Q and K at positions that restart with every sequence, attend,
+    differentiate, rotate the gradients back. Against the definitions in double end to end."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    lens, Hq, Hkv, d = [300, 5, 190], 4, 2, 64
+    cu, T, Q, K, V, dO = _batch(lens, 0, Hq, Hkv, d, F32, "nhd", 91)
+    pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32).cuda()
+    spec = P.rope_spec(d, 32, layout="interleaved", scaling="yarn", factor=2.0, trained=128)
+    freq, scale = ref.frequencies(32, 10000.0, "yarn", 2.0, 128)
+    Qr, Kr = torch.empty_like(Q), torch.empty_like(K)
+    P.rope_apply(spec, Q[None], K[None], Qr[None], Kr[None], pos=pos)
+    s, plan, O, lse = _forward(P, cu, T, Qr, Kr, V)
+    dQ, dK, dV = torch.empty_like(Q), torch.empty_like(K), torch.empty_like(V)
+    P.packed_backward(s, Qr, Kr, V, plan, O, lse, dO, torch.empty((Hq, T), device="cuda"), dQ, dK, dV)
+    P.rope_apply(spec, dQ[None], dK[None], dQ[None], dK[None], pos=pos, inverse=True)
+    q64, k64 = (ref.rope(x[None], pos[None], freq, scale, 32, "interleaved")[0] for x in (Q, K))
+    wo, _ = ref.packed(q64, k64, V, cu)
+    # the fp32 bounds above; the rotation adds 7e-7 relative per element, far below them
+    assert float((O.double() - wo).abs().max()) <= 2e-5 * float(V.abs().max())
+    want = list(ref.packed_grad(q64, k64, V, dO, cu))
+    for i in range(2):
+        want[i] = ref.rope(want[i][None], pos[None], freq, scale, 32, "interleaved", inverse=True)[0]
+    for got, w in zip((dQ, dK, dV), want):
+        assert float((got.double() - w).abs().max()) <= 2e-4 * float(w.abs().max())

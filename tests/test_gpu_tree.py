@@ -166,3 +166,111 @@ def test_tree_under_a_graph_with_new_lengths():
         graph.replay()
         torch.cuda.synchronize()
         _compare(O, lse, Q, K, V, new, chain)
+
+
+def test_a_cache_whose_offsets_pass_32_bits():
+    """Two sequences 2^32 elements apart, heads 2^31 apart, in a strided cache."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 26 GB of device memory")
+    N, d, T, lens = 400, 64, 3, [397, 130]
+    g = torch.Generator().manual_seed(47)
+    for dtype in (BF16,):
+        flat = [torch.empty(2 ** 32 + 2 ** 31 + N * d, dtype=dtype, device="cuda") for _ in range(2)]
+        K, V = (f.as_strided((2, 2, N, d), (2 ** 32, 2 ** 31, d, 1)) for f in flat)
+        Q = _tensor("hnd", 2, 4, T, d, dtype, g)
+        for x in (K, V):
+            x.copy_(torch.randn((2, 2, N, d), generator=g).to(dtype).cuda())
+        parent = [[-1, 0, 0], [-1, -1, 1]]
+        O, lse, status = _run(P, Q, K, V, lens, parent)
+        assert status == 0
+        _compare(O, lse, Q, K.contiguous(), V.contiguous(), lens, parent)
+
+
+def test_absent_sequences_may_hold_anything():
+    """A padded batch: sequences without tokens, their context rows NaN."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    g = torch.Generator().manual_seed(57)
+    for dtype in (F32, BF16):
+        Q, K, V = (_tensor("nhd", 3, H, n, 64, dtype, g) for H, n in ((4, 2), (2, 300), (2, 300)))
+        K[1], V[1] = float("nan"), float("nan")
+        parent = [[-1, 0], [-2, -2], [-1, -2]]
+        O, lse, status = _run(P, Q, K, V, [200, 250, 17], parent)
+        assert status == 0
+        assert (O[1] == 0).all() and (lse[1] == -float("inf")).all()
+        keep = [0, 2]
+        _compare(O[keep], lse[keep], Q[keep], K[keep], V[keep], [200, 17], [parent[0], parent[2]])
+
+
+def test_single_tokens_equal_the_dense_decode():
+    """One token per sequence at one length: the framework's dense decode attention of the same cache."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    g = torch.Generator().manual_seed(67)
+    B, Hq, Hkv, N, d = 3, 8, 2, 1000, 128
+    Q, K, V = (_tensor("hnd", B, H, n, d, BF16, g) for H, n in ((Hq, 1), (Hkv, N), (Hkv, N)))
+    O, lse, _ = _run(P, Q, K, V, [N - 1] * B, None)
+    s = P.make_shape(B, Hq, Hkv, N, 1, N - 1, d, 64, 4, 8, BF16)
+    O2, lse2 = torch.empty_like(O), torch.empty_like(lse)
+    P.dense_forward(s, Q, K, V, O2, lse2)
+    # both within half a bf16 step of the output and 2^-7 max|v| (P) of the same value
+    assert float((O.float() - O2.float()).abs().max()) <= 2.0 ** -6 * float(V.abs().max())
+    assert float((lse - lse2).abs().max()) <= 2e-4
+
+
+def test_two_calls_on_two_streams_with_workspaces_of_their_own():
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    g = torch.Generator().manual_seed(77)
+    jobs = []
+    for lens, T in (([3000, 10], 7), ([64, 2500], 30)):
+        Q, K, V = (_tensor("hnd", 2, H, n, 128, BF16, g) for H, n in ((8, T), (2, 3100), (2, 3100)))
+        s = P.tree_shape(2, 8, 2, 3100, T, 128, BF16)
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        want = _run(P, Q, K, V, lens, None)
+        jobs.append((torch.cuda.Stream(), s, Q, K, V, n, want,
+                     torch.empty(P.tree_workspace_bytes(s), dtype=torch.uint8, device="cuda"), torch.empty_like(Q),
+                     torch.empty((2, 8, T), device="cuda")))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, s, Q, K, V, n, want, ws, O, lse in jobs:
+            P.tree_forward(s, Q, K, V, n, None, O, lse, ws, stream=st)
+    torch.cuda.synchronize()
+    for st, s, Q, K, V, n, want, ws, O, lse in jobs:
+        assert torch.equal(O, want[0]) and torch.equal(lse, want[1])
+
+
+def test_drafts_rotated_at_their_depth_after_a_prompt():
+    """The operators as a server uses them: rotate and attend a prompt, keep its keys and values in a cache,
+    append a rotated tree at positions len + depth, attend the tree. The path through every token equals
+    causal attention of that path as a prompt."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    g = torch.Generator().manual_seed(87)
+    Hq, Hkv, d, n, N = 4, 2, 64, 150, 200
+    parent = [-1, 0, 0, 1, 2, 3]
+    T, depth = len(parent), [0, 1, 1, 2, 2, 3]
+    K, V = (torch.randn((1, Hkv, n + T, d), generator=g).cuda() for _ in range(2))
+    Q = torch.randn((1, Hq, n + T, d), generator=g).cuda()
+    pos = torch.tensor(list(range(n)) + [n + x for x in depth], dtype=torch.int32, device="cuda")
+    spec = P.rope_spec(d)
+    cache_k, cache_v = (torch.full((1, Hkv, N, d), float("nan"), device="cuda") for _ in range(2))
+    cache_v[:, :, :n + T] = V
+    Qr = torch.empty_like(Q)
+    P.rope_apply(spec, Q, K, Qr, cache_k[:, :, :n + T], pos=pos)
+    O, lse, status = _run(P, Qr[:, :, n:], cache_k, cache_v, [n], [parent])
+    assert status == 0
+    for t in range(T):
+        path = [t]
+        while parent[path[0]] >= 0:
+            path.insert(0, parent[path[0]])
+        rows = list(range(n)) + [n + u for u in path]
+        cu = [0, len(rows)]
+        s = P.packed_shape(1, len(rows), Hq, Hkv, d, F32)
+        plan = P.packed_plan(s, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        o = torch.empty((Hq, len(rows), d), device="cuda")
+        P.packed_forward(s, Qr[0, :, rows], cache_k[0, :, rows], cache_v[0, :, rows], plan, o)
+        # two fp32 evaluations, each within 2e-5 max|v| of the definition
+        assert float((o[:, -1] - O[0, :, t]).abs().max()) <= 4e-5 * float(V.abs().max())
