@@ -19,6 +19,12 @@
 //               warps a scheduler: with two, the waits and tensor-memory loads of a step were not covered
 //   warp 16     TMA      warp 17  products (S and dQ in the dQ kernel)      warp 18  dP in the dQ kernel
 //   warp 19     lse, delta and tails (dK/dV only)
+// delta = dO . O is taken from the rounded O. Where a row sees few keys, dP and delta nearly cancel (with one
+// key they are equal), and that rounding would be what is left. The rows of a sequence's first tile see one
+// key tile, so the dQ kernel has all of their P and dP at hand: it refines delta by one step,
+//   delta + sum_k P (dP - delta) = sum_k P dP up to the rounding of the difference alone,
+// and writes it back for the dK/dV kernel, which therefore runs second. Rows with more keys keep dO . O: their
+// O is an average, and its rounding small against dP.
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"
@@ -443,8 +449,9 @@ struct QPlan {
   static constexpr int TB = 128 * D * 2;
   static constexpr int NK = 3, NV = 2;  // K stages (a K tile lives until dQ has read it), V stages
   static constexpr int kQ = 0, kG = TB, kK = 2 * TB, kV = kK + NK * TB;
-  static constexpr int kBar = kV + NV * TB;
-  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 1 + 1 + 1 + 1 + 2;
+  static constexpr int kSum = kV + NV * TB;  // [128] fp32: row sums on their way through the warpgroups
+  static constexpr int kBar = kSum + 512;
+  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 1 + 1 + 1 + 1 + 2 + 16;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16 + 1024;
 };
@@ -489,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bar_acc_full = bar_dp_free + 1;
   uint64_t* bar_acc_free = bar_acc_full + 1;
   uint64_t* bar_drain = bar_acc_free + 1;  // [2]
+  uint64_t* bar_sum = bar_drain + 2;       // [4][4] rows, warpgroup: has added its part
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -513,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_ds_full + i, kSoftmax);
       mbar_init(bar_drain + i, 1);
     }
+    for (int i = 0; i < 16; i++) mbar_init(bar_sum + i, 1);
     mbar_init(bar_dp_full, 1);
     mbar_init(bar_dp_free, kSoftmax);
     mbar_init(bar_acc_full, 1);
@@ -659,13 +668,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
     const int rr = wq * 32 + lane;
     bool ok = true;
-    int items = 0, u = 0;
+    volatile float* sum = reinterpret_cast<volatile float*>(smem + PL::kSum) + rr;
+    int items = 0, u = 0, sums = 0;  // sums: rounds of the row sums so far
     for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       const int row = it.row0 + rr;
       const bool live = it.row0 + wq * 32 < it.end;
       const int64_t at = (int64_t)it.head * g.T + min(row, it.end - 1);
       const float nl = -kLog2e * a.lse[at], nd = -a.delta[at];
-      const float2 scl = make_float2(sl2, sl2), off = make_float2(nl, nl), del = make_float2(nd, nd);
+      const float2 scl = make_float2(sl2, sl2), off = make_float2(nl, nl);
+      float2 del = make_float2(nd, nd);
       for (int i = 0; i < it.steps; i++, u++) {
         const int b = u & 1;
         const bool diag = i == it.steps - 1;
@@ -698,6 +709,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               d[c] = wg * 32 + c <= rr ? d[c] : 0.f;
             }
           }
+          if (it.steps == 1) {
+            // this tile is all that the row sees: delta += sum_k P (dP - delta), the warpgroups in order
+            float part = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; c++) part = fmaf(p[c], d[c] + nd, part);
+            if (wg > 0) {
+              ok = warp_wait(bar_sum + 4 * wq + wg - 1, sums & 1, abort_flag);
+              part += *sum;
+            }
+            *sum = part;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_sum + 4 * wq + wg);
+            if (ok) ok = warp_wait(bar_sum + 4 * wq + 3, sums & 1, abort_flag);
+            sums++;
+            const float refined = -nd + *sum;
+            del = make_float2(-refined, -refined);
+            if (wg == 0 && row < it.end) a.delta[at] = refined;
+          }
 #pragma unroll
           for (int c = 0; c < 16; c++) {
             const float2 x =
@@ -709,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
+        if (!ok) break;
         if (lane == 0) {
           mbar_arrive(bar_dp_free);
           mbar_arrive(bar_ds_full + b);
@@ -745,18 +775,18 @@ cudaError_t launch_d(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st
       !make_tmap_bf16_view(&mv, a.v.data, a.v.batch, a.v.head, a.v.row, D, g.T, g.Hkv, 1, 128) ||
       !make_tmap_bf16_view(&mg, a.dout.data, a.dout.batch, a.dout.head, a.dout.row, D, g.T, g.Hq, 1, 128))
     return cudaErrorInvalidValue;
-  auto kk = packed_dkdv_tc_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, KPlan<D>::kBytes);
+  auto kq = packed_dq_tc_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, QPlan<D>::kBytes);
   if (e != cudaSuccess) return e;
-  int64_t items = packed_list_cap(g, kListK) * g.Hkv;
-  kk<<<(unsigned)(items < 148 ? items : 148), kThreads, KPlan<D>::kBytes, st>>>(mq, mk, mv, mg, g, a);
+  int64_t items = packed_list_cap(g, kListQ) * g.Hq;
+  kq<<<(unsigned)(items < 148 ? items : 148), kThreads, QPlan<D>::kBytes, st>>>(mq, mk, mv, mg, g, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto kq = packed_dq_tc_kernel<D>;
-  e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, QPlan<D>::kBytes);
+  auto kk = packed_dkdv_tc_kernel<D>;
+  e = cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, KPlan<D>::kBytes);
   if (e != cudaSuccess) return e;
-  items = packed_list_cap(g, kListQ) * g.Hq;
-  kq<<<(unsigned)(items < 148 ? items : 148), kThreads, QPlan<D>::kBytes, st>>>(mq, mk, mv, mg, g, a);
+  items = packed_list_cap(g, kListK) * g.Hkv;
+  kk<<<(unsigned)(items < 148 ? items : 148), kThreads, KPlan<D>::kBytes, st>>>(mq, mk, mv, mg, g, a);
   return cudaGetLastError();
 }
 

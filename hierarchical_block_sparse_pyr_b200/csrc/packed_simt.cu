@@ -150,7 +150,26 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        s[i][j] = k0 + tx + 16 * j <= row0 + 4 * ty + i ? exp2f(s[i][j] * sl2 - lse2[i]) * (dp[i][j] - del[i]) : 0.f;
+        s[i][j] = k0 + tx + 16 * j <= row0 + 4 * ty + i ? exp2f(s[i][j] * sl2 - lse2[i]) : 0.f;
+    if (stop - start <= kTile) {
+      // The row sees this tile alone, perhaps one key, where dP and delta cancel: delta += sum_k P (dP - delta),
+      // which is sum_k P dP up to the rounding of the difference. The dK/dV kernel, which runs second, reads it.
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) sum = fmaf(s[i][j], dp[i][j] - del[i], sum);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        del[i] += sum;
+        const int t = row0 + 4 * ty + i;
+        if (tx == 0 && t < end) a.delta[(int64_t)h * g.T + t] = del[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) s[i][j] *= dp[i][j] - del[i];
     __syncwarp();
     store_p(Ps, s);
     __syncwarp();
@@ -231,10 +250,10 @@ cudaError_t launch(K kern, int64_t blocks, int threads, int smem, const PackedGe
 
 template <typename T, int D>
 cudaError_t launch_bwd(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
-  const cudaError_t e = launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads,
-                               dq_smem<D>(), g, a, st);
+  const cudaError_t e =
+      launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads, dq_smem<D>(), g, a, st);
   if (e != cudaSuccess) return e;
-  return launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads, dq_smem<D>(), g, a, st);
+  return launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads, dq_smem<D>(), g, a, st);
 }
 
 }  // namespace

@@ -316,3 +316,38 @@ def test_rotate_attend_and_train_in_one_stream():
         want[i] = ref.rope(want[i][None], pos[None], freq, scale, 32, "interleaved", inverse=True)[0]
     for got, w in zip((dQ, dK, dV), want):
         assert float((got.double() - w).abs().max()) <= 2e-4 * float(w.abs().max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_single_tokens_have_no_score_gradient(dtype):
+    """A token alone in its sequence: dQ and dK are zero, exactly, and dV is dO summed over the group."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    for d in (64, 128):
+        cu, T, Q, K, V, dO = _batch([1] * 150, 0, 4, 2, d, dtype, "nhd", 95)
+        s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+        grads = [torch.full_like(x, 7.0) for x in (Q, K, V)]
+        P.packed_backward(s, Q, K, V, plan, O, lse, dO, torch.empty_like(lse), *grads)
+        assert (grads[0] == 0).all() and (grads[1] == 0).all()
+        want = dO.double().reshape(2, 2, T, d).sum(1)
+        # P = 1 up to a few fp32 roundings of the score; bf16: exactly 1, and one rounding of the output
+        eps = 2.0 ** -8 if dtype == BF16 else 2e-6
+        assert ((grads[2].double() - want).abs() <= eps * want.abs() + 2e-6 * dO.abs().max()).all()
+
+
+@pytest.mark.parametrize("lens", [[2] * 60, [3, 5, 2, 9, 4, 17, 1, 6], [40, 128, 100]])
+def test_gradients_of_short_sequences(lens):
+    """Few keys a row: dP and delta nearly cancel, and delta from a rounded O would leave its rounding. With delta
+    refined, dS carries its own rounding and those of the fp32 sums: the bf16 relative bound of the module holds."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    for d in (64, 128):
+        cu, T, Q, K, V, dO = _batch(lens, 3, 4, 2, d, BF16, "hnd", 96)
+        s, plan, O, lse = _forward(P, cu, T, Q, K, V)
+        grads = [torch.full_like(x, 7.0) for x in (Q, K, V)]
+        P.packed_backward(s, Q, K, V, plan, O, lse, dO, torch.empty_like(lse), *grads)
+        e = cu[-1]
+        want = ref.packed_grad(Q[:, :e], K[:, :e], V[:, :e], dO[:, :e], cu)
+        for got, w in zip(grads, want):
+            # two bf16 roundings, each at most 2^-8 of the value
+            assert float((got[:, :e].double() - w).norm() / w.norm()) <= 2 * 2.0 ** -8
