@@ -408,32 +408,30 @@ def _refuse(t, name, shape, dtype, device):
     raise ValueError(f"the elements of a row of {name} must be adjacent")
 
 
-def _views(dtype, device, operands):
+def _views(dtype, device, *operands):
     """pyr_views of (tensor, name, shape) operands, tensors [batch, head, row, d] or [head, row, d] of any
-    strides with adjacent elements: the array that holds them and their addresses."""
+    strides with adjacent elements: the array that holds them and its address (32 bytes a view)."""
     td = _TORCH_DTYPES.get(dtype)
     vals = []
     for t, name, shape in operands:
-        if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not td or t.get_device() != device or \
+        if not isinstance(t, torch.Tensor) or t.dtype is not td or t.shape != shape or t.get_device() != device or \
                 device < 0:
             _refuse(t, name, shape, td, device)
         st = t.stride()
         if st[-1] != 1:
             _refuse(t, name, shape, td, device)
-        vals += (t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
-    n = len(vals) // 4
-    arr = _VIEW_ARRAYS[n](*vals)
-    base = ctypes.addressof(arr)
-    return arr, [base + 32 * i for i in range(n)]
+        vals += (t.data_ptr(), *st[:3]) if len(st) == 4 else (t.data_ptr(), 0, st[0], st[1])
+    arr = _VIEW_ARRAYS[len(operands)](*vals)
+    return arr, ctypes.addressof(arr)
 
 
 def _device_of(t):
     return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
-def _plain(t, name, dtype, numel, device, nullable=False):
-    """Pointer of a contiguous tensor of one dtype with at least numel elements."""
-    if t is None and nullable:
+def _plain(t, name, dtype, numel, device):
+    """Pointer of a contiguous tensor of one dtype with at least numel elements (None: NULL)."""
+    if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -446,13 +444,18 @@ def _plain(t, name, dtype, numel, device, nullable=False):
     return t.data_ptr()
 
 
+def _need(t, name, dtype, numel, device):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return _plain(t, name, dtype, numel, device)
+
+
 def _call(fn, what, device, stream, *args):
     """fn(*args, stream) with the operands' device current; stream None: that device's current stream."""
     if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
             return _call(fn, what, device, stream, *args)
-    raw = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
-    rc = fn(*args, raw)
+    rc = fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
     if rc:
         raise PyrError(rc, what)
 
@@ -498,17 +501,18 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
         heads[i] = x.shape[1]
         shape = (B, heads[i], N, d)
         operands += ((x, name, shape), (y, name + "o", shape))
-    arr, v = _views(dt, dev, operands)
-    q, qo = (v[0], v[1]) if Q is not None else (None, None)
-    k, ko = (v[-2], v[-1]) if K is not None else (None, None)
+    arr, v = _views(dt, dev, *operands)
+    q, qo = (v, v + 32) if Q is not None else (None, None)
+    v += 64 if Q is not None else 0
+    k, ko = (v, v + 32) if K is not None else (None, None)
     stride = 0
-    p = _plain(pos, "pos", torch.int32, 0, dev, True)
+    p = _plain(pos, "pos", torch.int32, 0, dev)
     if pos is not None:
         if pos.shape != (B, N) and pos.shape != (N,):
             raise ValueError("pos must be [B, N] or [N]")
         stride = N if pos.dim() == 2 else 0
     _call(_L().rope_apply, "rope_apply", dev, stream, ctypes.byref(spec), B, heads[0], heads[1], N, dt, q, k, p, stride,
-          int(pos_offset), qo, ko, int(bool(inverse)), _plain(status, "status", torch.int32, 1, dev, True))
+          int(pos_offset), qo, ko, int(bool(inverse)), _plain(status, "status", torch.int32, 1, dev))
 
 
 def packed_shape(S: int, T: int, Hq: int, Hkv: int, d: int, dtype) -> PackedShape:
@@ -520,18 +524,27 @@ def packed_plan_elems(s: PackedShape) -> int:
     return _L().packed_plan_elems(ctypes.byref(s))
 
 
+def _plan_words(s):
+    """packed_plan_elems, asked of the library once per shape and its values."""
+    key = (s.S, s.T, s.Hq, s.Hkv, s.d, s.dtype)
+    known = getattr(s, "_words", None)
+    if known is None or known[0] != key:
+        known = s._words = (key, packed_plan_elems(s))
+    return known[1]
+
+
 def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
     """The work list of sequences [cu[i], cu[i+1]) (int32 CUDA tensor [S + 1]); it serves every packed_forward
     and packed_backward of this shape and these boundaries. Returns plan (allocated if None)."""
     dev = _device_of(cu)
-    c = _plain(cu, "cu", torch.int32, s.S + 1, dev)
+    c = _need(cu, "cu", torch.int32, s.S + 1, dev)
     n = packed_plan_elems(s)
     if plan is None:
         plan = torch.empty(max(n, 1), dtype=torch.int32, device=cu.device)
         if isinstance(stream, torch.cuda.Stream):
             plan.record_stream(stream)
     _call(_L().packed_plan, "packed_plan", dev, stream, ctypes.byref(s), c,
-          _plain(plan, "plan", torch.int32, n, dev), _plain(status, "status", torch.int32, 1, dev, True))
+          _need(plan, "plan", torch.int32, n, dev), _plain(status, "status", torch.int32, 1, dev))
     return plan
 
 
@@ -540,11 +553,10 @@ def packed_forward(s: PackedShape, Q, K, V, plan, O, lse=None, status=None, stre
     [Hq, T]. Tokens outside the sequences are neither used nor written."""
     dev = _device_of(Q)
     q, kv = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d)
-    arr, v = _views(s.dtype, dev, ((Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q)))
-    _call(_L().packed_forward, "packed_forward", dev, stream, ctypes.byref(s), v[0], v[1], v[2],
-          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), v[3],
-          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev, True),
-          _plain(status, "status", torch.int32, 1, dev, True))
+    arr, v = _views(s.dtype, dev, (Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q))
+    _call(_L().packed_forward, "packed_forward", dev, stream, ctypes.byref(s), v, v + 32, v + 64,
+          _need(plan, "plan", torch.int32, _plan_words(s), dev), v + 96,
+          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev), _plain(status, "status", torch.int32, 1, dev))
 
 
 def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV, status=None, stream=None):
@@ -552,13 +564,13 @@ def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV
     fp32 workspace [Hq, T]."""
     dev = _device_of(Q)
     q, kv = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d)
-    arr, v = _views(s.dtype, dev, ((Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q), (dO, "dO", q), (dQ, "dQ", q),
-                                   (dK, "dK", kv), (dV, "dV", kv)))
-    _call(_L().packed_backward, "packed_backward", dev, stream, ctypes.byref(s), v[0], v[1], v[2],
-          _plain(plan, "plan", torch.int32, packed_plan_elems(s), dev), v[3],
-          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev), v[4],
-          _plain(delta, "delta", torch.float32, s.Hq * s.T, dev), v[5], v[6], v[7],
-          _plain(status, "status", torch.int32, 1, dev, True))
+    arr, v = _views(s.dtype, dev, (Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q), (dO, "dO", q), (dQ, "dQ", q),
+                    (dK, "dK", kv), (dV, "dV", kv))
+    n = s.Hq * s.T
+    _call(_L().packed_backward, "packed_backward", dev, stream, ctypes.byref(s), v, v + 32, v + 64,
+          _need(plan, "plan", torch.int32, _plan_words(s), dev), v + 96, _need(lse, "lse", torch.float32, n, dev),
+          v + 128, _need(delta, "delta", torch.float32, n, dev), v + 160, v + 192, v + 224,
+          _plain(status, "status", torch.int32, 1, dev))
 
 
 def tree_shape(B: int, Hq: int, Hkv: int, N: int, T: int, d: int, dtype) -> TreeShape:
@@ -576,12 +588,12 @@ def tree_forward(s: TreeShape, Q, K, V, lens, parent, O, lse=None, workspace=Non
     values are in the cache rows lens[b] + t. workspace: a CUDA uint8 tensor of tree_workspace_bytes(s) bytes."""
     dev = _device_of(Q)
     q, kv = (s.B, s.Hq, s.T, s.d), (s.B, s.Hkv, s.N, s.d)
-    arr, v = _views(s.dtype, dev, ((Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q)))
-    w = _plain(workspace, "workspace", torch.uint8, 0, dev)
-    _call(_L().tree_forward, "tree_forward", dev, stream, ctypes.byref(s), v[0], v[1], v[2],
-          _plain(lens, "lens", torch.int32, s.B, dev), _plain(parent, "parent", torch.int32, s.B * s.T, dev, True), v[3],
-          _plain(lse, "lse", torch.float32, s.B * s.Hq * s.T, dev, True), w, workspace.numel(),
-          _plain(status, "status", torch.int32, 1, dev, True))
+    arr, v = _views(s.dtype, dev, (Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q))
+    w = _need(workspace, "workspace", torch.uint8, 0, dev)
+    _call(_L().tree_forward, "tree_forward", dev, stream, ctypes.byref(s), v, v + 32, v + 64,
+          _need(lens, "lens", torch.int32, s.B, dev), _plain(parent, "parent", torch.int32, s.B * s.T, dev), v + 96,
+          _plain(lse, "lse", torch.float32, s.B * s.Hq * s.T, dev), w, workspace.numel(),
+          _plain(status, "status", torch.int32, 1, dev))
 
 
 def selftest_wait(status, stream=None):
