@@ -102,10 +102,10 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
                      __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
-// 2^x of the c-th pair of a row: OF16 of 16 pairs on the FMA pipe, evenly spread, the others on MUFU
-template <int OF16, int DEG>
+// 2^x of the c-th of N pairs: the last FMA of them on the FMA pipe, the others on MUFU
+template <int N, int FMA, int DEG>
 __device__ __forceinline__ float2 exp2_mix(int c, float2 x) {
-  if ((c + 1) * OF16 / 16 != c * OF16 / 16) return exp2_fma<DEG>(x);
+  if (c >= N - FMA) return exp2_fma<DEG>(x);
   return make_float2(ex2(x.x), ex2(x.y));
 }
 
