@@ -1,10 +1,13 @@
 // Causal attention of packed prompts and its gradients on the CUDA cores, fp32 arithmetic throughout: the
 // fp32 path (reduced-precision tensor-core operands would lose what fp32 callers keep).
 //
-// Forward and dQ: one CTA of 128 threads per (32-row tile, query head), walking the keys up to the tile's end.
-// dK/dV: one per (32-key tile, key/value head), walking the rows from the tile's start on, over the heads of
-// its group, so that every gradient is summed by one CTA in a fixed order. Tiles come longest first from the
-// plan. 32 rows rather than 64: a CTA's walk is the longest chain of the call, and two to five CTAs share an SM. Rows behind the sequence's end are loaded as zeros, never from memory.
+// Forward and dQ: one CTA per (32-row tile, query head), walking the keys up to the tile's end. dK/dV: one per
+// (32-key tile, key/value head), walking the rows from the tile's start on, over the heads of its group, so
+// that every gradient is summed by one CTA in a fixed order. Tiles come longest first from the plan.
+// A CTA is two teams of 128 threads that take the even and the odd steps of its walk with sums of their own,
+// added (team 0 + team 1) at the end: the longest walk bounds small calls, and this halves it (2 heads of 64,
+// 4K tokens, gradients: 450 -> 330 us).
+// Rows behind the sequence's end are loaded as zeros, never from memory.
 #include "packed.cuh"
 #include "simt_tile.cuh"
 
@@ -15,27 +18,47 @@ namespace {
 using namespace simt;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kRows = 32;  // rows of a tile, packed_tile_rows() of fp32
-constexpr int kThreads = 4 * kRows;
+constexpr int kRows = 32;         // rows of a tile, packed_tile_rows() of fp32
+constexpr int kTeam = 4 * kRows;  // threads of a team
+constexpr int kThreads = 2 * kTeam;
+
+__device__ __forceinline__ int team() { return threadIdx.x / kTeam; }
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team()), "n"(kTeam) : "memory"); }
+
+// team 1's 32 x D sums on their way to team 0, in shared memory that both have finished with
+template <int D>
+__device__ __forceinline__ void put_acc(float* buf, const float (&acc)[4][D / 16]) {
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) buf[(i * (D / 16) + c) * kTeam + team_tid<kTeam>()] = acc[i][c];
+}
+template <int D>
+__device__ __forceinline__ float got_acc(const float* buf, int i, int c) {
+  return buf[(i * (D / 16) + c) * kTeam + team_tid<kTeam>()];
+}
 
 template <int D>
+constexpr int fwd_team() { return kTile * (D + 4) + kTile * D; }  // K (P over K), V
+template <int D>
 constexpr int fwd_smem() {
-  return ((kRows + kTile) * (D + 4) + kTile * D) * 4;  // Q, K (P over K), V
+  return (kRows * (D + 4) + 2 * fwd_team<D>()) * 4;  // Q, and the teams' tiles
 }
 
 // S = Q K^T, online softmax, O += P V over 64-key tiles; P goes over K's buffer.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float *Qs = sm, *Ks = Qs + kRows * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
+  float *Qs = sm, *Ks = Qs + kRows * (D + 4) + team() * fwd_team<D>(), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
   if (tile >= packed_tiles(g, a.plan, kListFwd, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListFwd))[tile];
   const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float sl2 = rsqrtf((float)D) * kLog2e;
   const int nrow = min(kRows, end - row0);
-  load_rows<T, D, kRows>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<kThreads, T, D, kRows>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  __syncthreads();
   float m[4], l[4], acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -45,30 +68,49 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
     for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
   }
   const int stop = row0 + nrow;
-  for (int k0 = start; k0 < stop; k0 += kTile) {
+  for (int k0 = start + team() * kTile; k0 < stop; k0 += 2 * kTile) {
     const int nk = min(kTile, stop - k0);
-    __syncthreads();
-    load_rows<T, D, kTile>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
-    load_rows<T, D, kTile>(Vs, D, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
-    __syncthreads();
+    team_sync();
+    load_rows<kTeam, T, D, kTile>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<kTeam, T, D, kTile>(Vs, D, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    team_sync();
     float s[4][4];
-    mul_nt<D>(s, Qs, D + 4, Ks, D + 4);
+    mul_nt<kTeam, D>(s, Qs, D + 4, Ks, D + 4);
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++) s[i][j] = k0 + tx + 16 * j <= row0 + 4 * ty + i ? s[i][j] * sl2 : -INFINITY;
     softmax_step<D>(s, m, l, acc);
-    __syncthreads();  // every thread is done with K
-    store_p(Ps, s);
+    team_sync();  // every thread is done with K
+    store_p<kTeam>(Ps, s);
     __syncwarp();  // a row of P is written and read by one half-warp
-    mul_acc<D>(acc, Ps, Vs, D);
+    mul_acc<kTeam, D>(acc, Ps, Vs, D);
   }
+  __syncthreads();
+  float* buf = sm;  // 32 x D sums, then maximum and sum of the rows (each thread's own copy)
+  constexpr int kMl = kRows * D;
+  if (team() == 1) {
+    put_acc<D>(buf, acc);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      buf[kMl + (2 * i) * kTeam + team_tid<kTeam>()] = m[i];
+      buf[kMl + (2 * i + 1) * kTeam + team_tid<kTeam>()] = l[i];
+    }
+  }
+  __syncthreads();
+  if (team() == 1) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int t = row0 + 4 * ty + i;
     if (t >= end) continue;
-    store_row<T, D>(view_at<T>(a.o, 0, h, t), acc[i], 1.f / l[i]);
-    if (a.lse && tx == 0) a.lse[(int64_t)h * g.T + t] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
+    // team 0 has seen the first tile, which every row sees; team 1 may have seen nothing (m = -inf)
+    const float m1 = buf[kMl + (2 * i) * kTeam + team_tid<kTeam>()];
+    const float mm = fmaxf(m[i], m1), f0 = exp2f(m[i] - mm), f1 = exp2f(m1 - mm);
+    const float sum = l[i] * f0 + buf[kMl + (2 * i + 1) * kTeam + team_tid<kTeam>()] * f1;
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) acc[i][c] = acc[i][c] * f0 + got_acc<D>(buf, i, c) * f1;
+    store_row<T, D>(view_at<T>(a.o, 0, h, t), acc[i], 1.f / sum);
+    if (a.lse && tx == 0) a.lse[(int64_t)h * g.T + t] = (mm + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -108,8 +150,10 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(PackedGeo g, PackedBw
 }
 
 template <int D>
-constexpr int dq_smem() {
-  return (2 * (kRows + kTile) * (D + 4) + kRows * kPitchP) * 4;  // two operands each way, P or dS
+constexpr int bwd_team() { return 2 * kTile * (D + 4) + kRows * kPitchP; }  // a tile of two operands, P or dS
+template <int D>
+constexpr int bwd_smem() {
+  return (2 * kRows * (D + 4) + 2 * bwd_team<D>()) * 4;  // two operands of the CTA's rows, and the teams' tiles
 }
 
 // dS = P (dO V^T - delta), dQ += dS K
@@ -117,16 +161,17 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
-  float *Qs = sm, *Gs = Qs + kRows * P, *Ks = Gs + kRows * P, *Vs = Ks + kTile * P, *Ps = Vs + kTile * P;
+  float *Qs = sm, *Gs = Qs + kRows * P, *Ks = Gs + kRows * P + team() * bwd_team<D>(), *Vs = Ks + kTile * P,
+        *Ps = Vs + kTile * P;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
   if (tile >= packed_tiles(g, a.plan, kListQ, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
   const int start = w.x, end = w.y, row0 = w.z, hk = h / g.G;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
   const int nrow = min(kRows, end - row0);
-  load_rows<T, D, kRows>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
-  load_rows<T, D, kRows>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
+  load_rows<kThreads, T, D, kRows>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<kThreads, T, D, kRows>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
   float lse2[4], del[4], acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -136,16 +181,17 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
 #pragma unroll
     for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
   }
+  __syncthreads();
   const int stop = row0 + nrow;
-  for (int k0 = start; k0 < stop; k0 += kTile) {
+  for (int k0 = start + team() * kTile; k0 < stop; k0 += 2 * kTile) {
     const int nk = min(kTile, stop - k0);
-    __syncthreads();
-    load_rows<T, D, kTile>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
-    load_rows<T, D, kTile>(Vs, P, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
-    __syncthreads();
+    team_sync();
+    load_rows<kTeam, T, D, kTile>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<kTeam, T, D, kTile>(Vs, P, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    team_sync();
     float s[4][4], dp[4][4];
-    mul_nt<D>(s, Qs, P, Ks, P);
-    mul_nt<D>(dp, Gs, P, Vs, P);
+    mul_nt<kTeam, D>(s, Qs, P, Ks, P);
+    mul_nt<kTeam, D>(dp, Gs, P, Vs, P);
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
@@ -170,14 +216,21 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++) s[i][j] *= dp[i][j] - del[i];
+    store_p<kTeam>(Ps, s);
     __syncwarp();
-    store_p(Ps, s);
+    mul_acc<kTeam, D>(acc, Ps, Ks, P);
     __syncwarp();
-    mul_acc<D>(acc, Ps, Ks, P);
   }
+  __syncthreads();
+  if (team() == 1) put_acc<D>(sm, acc);
+  __syncthreads();
+  if (team() == 1) return;
 #pragma unroll
-  for (int i = 0; i < 4; i++)
+  for (int i = 0; i < 4; i++) {
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) acc[i][c] += got_acc<D>(sm, i, c);
     if (row0 + 4 * ty + i < end) store_row<T, D>(view_at<T>(a.dq, 0, h, row0 + 4 * ty + i), acc[i], scale);
+  }
 }
 
 // rows = keys, columns = queries: dV += P^T dO, dK += dS^T Q over the rows of the group's heads
@@ -185,53 +238,67 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
-  float *Ks = sm, *Vs = Ks + kRows * P, *Qs = Vs + kRows * P, *Gs = Qs + kTile * P, *Ps = Gs + kTile * P;
+  float *Ks = sm, *Vs = Ks + kRows * P, *Qs = Vs + kRows * P + team() * bwd_team<D>(), *Gs = Qs + kTile * P,
+        *Ps = Gs + kTile * P;
   const int tile = blockIdx.x / g.Hkv, hk = blockIdx.x - tile * g.Hkv;
   if (tile >= packed_tiles(g, a.plan, kListK, a.status)) return;
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListK))[tile];
   const int end = w.y, key0 = w.z;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
   const int nk = min(kRows, end - key0);
-  load_rows<T, D, kRows>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
-  load_rows<T, D, kRows>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
+  load_rows<kThreads, T, D, kRows>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
+  load_rows<kThreads, T, D, kRows>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
+  __syncthreads();
   float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++)
 #pragma unroll
     for (int c = 0; c < D / 16; c++) dk[i][c] = dv[i][c] = 0.f;
-  for (int h = hk * g.G; h < (hk + 1) * g.G; h++) {
-    for (int q0 = key0; q0 < end; q0 += kTile) {
-      const int nq = min(kTile, end - q0);
-      __syncthreads();
-      load_rows<T, D, kTile>(Qs, P, view_at<T>(a.q, 0, h, q0), a.q.row, nq);
-      load_rows<T, D, kTile>(Gs, P, view_at<T>(a.dout, 0, h, q0), a.dout.row, nq);
-      __syncthreads();
-      float s[4][4], dp[4][4];
-      mul_nt<D>(s, Ks, P, Qs, P);
-      mul_nt<D>(dp, Vs, P, Gs, P);
+  const int nq_tiles = (end - key0 + kTile - 1) / kTile, steps = nq_tiles * g.G;
+  for (int step = team(); step < steps; step += 2) {
+    const int h = hk * g.G + step / nq_tiles, q0 = key0 + step % nq_tiles * kTile;
+    const int nq = min(kTile, end - q0);
+    team_sync();
+    load_rows<kTeam, T, D, kTile>(Qs, P, view_at<T>(a.q, 0, h, q0), a.q.row, nq);
+    load_rows<kTeam, T, D, kTile>(Gs, P, view_at<T>(a.dout, 0, h, q0), a.dout.row, nq);
+    team_sync();
+    float s[4][4], dp[4][4];
+    mul_nt<kTeam, D>(s, Ks, P, Qs, P);
+    mul_nt<kTeam, D>(dp, Vs, P, Gs, P);
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int t = q0 + tx + 16 * j, tc = min(t, end - 1);
-        const float lse2 = a.lse[(int64_t)h * g.T + tc] * kLog2e, del = a.delta[(int64_t)h * g.T + tc];
+    for (int j = 0; j < 4; j++) {
+      const int t = q0 + tx + 16 * j, tc = min(t, end - 1);
+      const float lse2 = a.lse[(int64_t)h * g.T + tc] * kLog2e, del = a.delta[(int64_t)h * g.T + tc];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          s[i][j] = key0 + 4 * ty + i <= t && t < end ? exp2f(s[i][j] * sl2 - lse2) : 0.f;
-          dp[i][j] = s[i][j] * (dp[i][j] - del);
-        }
+      for (int i = 0; i < 4; i++) {
+        s[i][j] = key0 + 4 * ty + i <= t && t < end ? exp2f(s[i][j] * sl2 - lse2) : 0.f;
+        dp[i][j] = s[i][j] * (dp[i][j] - del);
       }
-      store_p(Ps, s);
-      __syncwarp();
-      mul_acc<D>(dv, Ps, Gs, P);
-      __syncwarp();
-      store_p(Ps, dp);
-      __syncwarp();
-      mul_acc<D>(dk, Ps, Qs, P);
-      __syncwarp();
     }
+    store_p<kTeam>(Ps, s);
+    __syncwarp();
+    mul_acc<kTeam, D>(dv, Ps, Gs, P);
+    __syncwarp();
+    store_p<kTeam>(Ps, dp);
+    __syncwarp();
+    mul_acc<kTeam, D>(dk, Ps, Qs, P);
+    __syncwarp();
   }
+  __syncthreads();
+  if (team() == 1) {
+    put_acc<D>(sm, dk);
+    put_acc<D>(sm + kRows * D, dv);
+  }
+  __syncthreads();
+  if (team() == 1) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
+#pragma unroll
+    for (int c = 0; c < D / 16; c++) {
+      dk[i][c] += got_acc<D>(sm, i, c);
+      dv[i][c] += got_acc<D>(sm + kRows * D, i, c);
+    }
     if (4 * ty + i >= nk) continue;
     store_row<T, D>(view_at<T>(a.dk, 0, hk, key0 + 4 * ty + i), dk[i], scale);
     store_row<T, D>(view_at<T>(a.dv, 0, hk, key0 + 4 * ty + i), dv[i], 1.f);
@@ -251,9 +318,9 @@ cudaError_t launch(K kern, int64_t blocks, int threads, int smem, const PackedGe
 template <typename T, int D>
 cudaError_t launch_bwd(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
   const cudaError_t e =
-      launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads, dq_smem<D>(), g, a, st);
+      launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads, bwd_smem<D>(), g, a, st);
   if (e != cudaSuccess) return e;
-  return launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads, dq_smem<D>(), g, a, st);
+  return launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads, bwd_smem<D>(), g, a, st);
 }
 
 }  // namespace

@@ -1,4 +1,5 @@
-// ROWS x 64 tiles of fp32 attention on the CUDA cores, 4 ROWS threads. Thread (tx, ty) = (tid % 16, tid / 16)
+// ROWS x 64 tiles of fp32 attention on the CUDA cores by a team of NT = 4 ROWS threads (a block may hold
+// several teams, each of consecutive threads). Thread (tx, ty) = (tid % 16, tid / 16) of its team
 // owns rows 4 ty .. 4 ty + 3 of every product; of a ROWS x 64 product it owns the columns tx + 16 j (four,
 // which keeps the 16-byte reads of the other operand's rows conflict-free with a row pitch of D + 4), of a
 // ROWS x D product the columns 4 tx + 64 j .. + 3. Rows of the result are written and read by one half-warp.
@@ -12,11 +13,15 @@ namespace simt {
 constexpr int kTile = 64;            // columns of a step
 constexpr int kPitchP = kTile + 4;
 
+template <int NT>
+__device__ __forceinline__ int team_tid() { return threadIdx.x & (NT - 1); }
+
 // dst[r][0 .. D) = row r of src where wanted(r), zeros in the other of the N rows
-template <typename T, int D, int N, typename F>
+template <int NT, typename T, int D, int N, typename F>
 __device__ __forceinline__ void load_rows_if(float* dst, int pitch, const T* src, int64_t stride, F wanted) {
   constexpr int E = 16 / sizeof(T), C = D / E;
-  for (int x = threadIdx.x; x < N * C; x += blockDim.x) {
+#pragma unroll 4
+  for (int x = team_tid<NT>(); x < N * C; x += NT) {
     const int r = x / C, c = x - r * C;
     float* d = dst + r * pitch + c * E;
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -34,15 +39,15 @@ __device__ __forceinline__ void load_rows_if(float* dst, int pitch, const T* src
   }
 }
 
-template <typename T, int D, int N>
+template <int NT, typename T, int D, int N>
 __device__ __forceinline__ void load_rows(float* dst, int pitch, const T* src, int64_t stride, int n) {
-  load_rows_if<T, D, N>(dst, pitch, src, stride, [n](int r) { return r < n; });
+  load_rows_if<NT, T, D, N>(dst, pitch, src, stride, [n](int r) { return r < n; });
 }
 
 // acc[i][j] = A[4 ty + i] . B[tx + 16 j] over D elements
-template <int D>
+template <int NT, int D>
 __device__ __forceinline__ void mul_nt(float (&acc)[4][4], const float* A, int pa, const float* B, int pb) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = team_tid<NT>() >> 4;
   float2 sum[4][4];  // of the even and of the odd elements
 #pragma unroll
   for (int i = 0; i < 4; i++)
@@ -70,9 +75,9 @@ __device__ __forceinline__ void mul_nt(float (&acc)[4][4], const float* A, int p
 }
 
 // acc[i][4 j + c] += sum_k P[4 ty + i][k] V[k][4 tx + 64 j + c], k = 0 .. 63
-template <int D>
+template <int NT, int D>
 __device__ __forceinline__ void mul_acc(float (&acc)[4][D / 16], const float* P, const float* V, int pv) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = team_tid<NT>() >> 4;
 #pragma unroll 2
   for (int k = 0; k < kTile; k += 4) {
     float p[4][4];
@@ -97,8 +102,9 @@ __device__ __forceinline__ void mul_acc(float (&acc)[4][D / 16], const float* P,
   }
 }
 
+template <int NT>
 __device__ __forceinline__ void store_p(float* P, const float (&s)[4][4]) {
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = threadIdx.x & 15, ty = team_tid<NT>() >> 4;
 #pragma unroll
   for (int i = 0; i < 4; i++)
 #pragma unroll

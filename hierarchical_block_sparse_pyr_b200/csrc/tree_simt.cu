@@ -61,11 +61,11 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
         return good && (u < 0 || (u < g.T && ((used >> u) & 1)));
       };
       __syncthreads();
-      load_rows_if<T, D, kTile>(Ks, D + 4, view_at<T>(a.k, b, hk, k0), a.k.row, wanted);
-      load_rows_if<T, D, kTile>(Vs, D, view_at<T>(a.v, b, hk, k0), a.v.row, wanted);
+      load_rows_if<4 * ROWS, T, D, kTile>(Ks, D + 4, view_at<T>(a.k, b, hk, k0), a.k.row, wanted);
+      load_rows_if<4 * ROWS, T, D, kTile>(Vs, D, view_at<T>(a.v, b, hk, k0), a.v.row, wanted);
       __syncthreads();
       float s[4][4];
-      mul_nt<D>(s, Qs, D + 4, Ks, D + 4);
+      mul_nt<4 * ROWS, D>(s, Qs, D + 4, Ks, D + 4);
 #pragma unroll
       for (int i = 0; i < 4; i++)
 #pragma unroll
@@ -73,9 +73,9 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
           s[i][j] = tree_sees(k0 + tx + 16 * j, len, mask[i]) && good ? s[i][j] * sl2 : -INFINITY;
       softmax_step<D>(s, m, l, acc);
       __syncthreads();
-      store_p(Ps, s);
+      store_p<4 * ROWS>(Ps, s);
       __syncwarp();
-      mul_acc<D>(acc, Ps, Vs, D);
+      mul_acc<4 * ROWS, D>(acc, Ps, Vs, D);
     }
     const bool whole = pc.whole;
     const int64_t part = (int64_t)(blockIdx.x * 2 + pc.part) * g.RR;
