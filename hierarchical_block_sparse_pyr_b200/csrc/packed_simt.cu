@@ -4,9 +4,9 @@
 // Forward and dQ: one CTA per (32-row tile, query head), walking the keys up to the tile's end. dK/dV: one per
 // (32-key tile, key/value head), walking the rows from the tile's start on, over the heads of its group, so
 // that every gradient is summed by one CTA in a fixed order. Tiles come longest first from the plan.
-// A CTA is two teams of 128 threads that take the even and the odd steps of its walk with sums of their own,
-// added (team 0 + team 1) at the end: the longest walk bounds small calls, and this halves it (2 heads of 64,
-// 4K tokens, gradients: 450 -> 330 us).
+// A CTA is two (d = 128) or four (d = 64) teams of 128 threads that take the steps of its walk in turn with sums
+// of their own, added in the teams' order at the end: the longest walk bounds small calls (2 heads of 64, 4K
+// tokens, gradients: one team 450 us, two 267, four 231).
 // Rows behind the sequence's end are loaded as zeros, never from memory.
 #include "packed.cuh"
 #include "simt_tile.cuh"
@@ -20,12 +20,15 @@ using namespace simt;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 32;         // rows of a tile, packed_tile_rows() of fp32
 constexpr int kTeam = 4 * kRows;  // threads of a team
-constexpr int kThreads = 2 * kTeam;
+template <int D>
+constexpr int kTeams = D == 64 ? 4 : 2;  // as many as shared memory holds
+template <int D>
+constexpr int kThreads = kTeams<D> * kTeam;
 
 __device__ __forceinline__ int team() { return threadIdx.x / kTeam; }
 __device__ __forceinline__ void team_sync() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team()), "n"(kTeam) : "memory"); }
 
-// team 1's 32 x D sums on their way to team 0, in shared memory that both have finished with
+// the teams' 32 x D sums on their way to team 0, in shared memory that all have finished with
 template <int D>
 __device__ __forceinline__ void put_acc(float* buf, const float (&acc)[4][D / 16]) {
 #pragma unroll
@@ -42,12 +45,12 @@ template <int D>
 constexpr int fwd_team() { return kTile * (D + 4) + kTile * D; }  // K (P over K), V
 template <int D>
 constexpr int fwd_smem() {
-  return (kRows * (D + 4) + 2 * fwd_team<D>()) * 4;  // Q, and the teams' tiles
+  return (kRows * (D + 4) + kTeams<D> * fwd_team<D>()) * 4;  // Q, and the teams' tiles
 }
 
 // S = Q K^T, online softmax, O += P V over 64-key tiles; P goes over K's buffer.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
+__global__ void __launch_bounds__(kThreads<D>) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm, *Ks = Qs + kRows * (D + 4) + team() * fwd_team<D>(), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
   const int tile = blockIdx.x / g.Hq, h = blockIdx.x - tile * g.Hq;
@@ -57,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
   const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float sl2 = rsqrtf((float)D) * kLog2e;
   const int nrow = min(kRows, end - row0);
-  load_rows<kThreads, T, D, kRows>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<kThreads<D>, T, D, kRows>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
   __syncthreads();
   float m[4], l[4], acc[4][D / 16];
 #pragma unroll
@@ -68,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
     for (int c = 0; c < D / 16; c++) acc[i][c] = 0.f;
   }
   const int stop = row0 + nrow;
-  for (int k0 = start + team() * kTile; k0 < stop; k0 += 2 * kTile) {
+  for (int k0 = start + team() * kTile; k0 < stop; k0 += kTeams<D> * kTile) {
     const int nk = min(kTile, stop - k0);
     team_sync();
     load_rows<kTeam, T, D, kTile>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
@@ -87,9 +90,10 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
     mul_acc<kTeam, D>(acc, Ps, Vs, D);
   }
   __syncthreads();
-  float* buf = sm;  // 32 x D sums, then maximum and sum of the rows (each thread's own copy)
-  constexpr int kMl = kRows * D;
-  if (team() == 1) {
+  // per team behind the first: 32 x D sums, then maximum and sum of the rows (each thread's own copy)
+  constexpr int kMl = kRows * D, kPart = kMl + 8 * kTeam;
+  if (team() > 0) {
+    float* buf = sm + (team() - 1) * kPart;
     put_acc<D>(buf, acc);
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -98,19 +102,24 @@ __global__ void __launch_bounds__(kThreads) packed_fwd_simt_kernel(PackedGeo g, 
     }
   }
   __syncthreads();
-  if (team() == 1) return;
+  if (team() > 0) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     const int t = row0 + 4 * ty + i;
     if (t >= end) continue;
-    // team 0 has seen the first tile, which every row sees; team 1 may have seen nothing (m = -inf)
-    const float m1 = buf[kMl + (2 * i) * kTeam + team_tid<kTeam>()];
-    const float mm = fmaxf(m[i], m1), f0 = exp2f(m[i] - mm), f1 = exp2f(m1 - mm);
-    const float sum = l[i] * f0 + buf[kMl + (2 * i + 1) * kTeam + team_tid<kTeam>()] * f1;
+    // team 0 has seen the first tile, which every row sees; the others may have seen nothing (m = -inf)
 #pragma unroll
-    for (int c = 0; c < D / 16; c++) acc[i][c] = acc[i][c] * f0 + got_acc<D>(buf, i, c) * f1;
-    store_row<T, D>(view_at<T>(a.o, 0, h, t), acc[i], 1.f / sum);
-    if (a.lse && tx == 0) a.lse[(int64_t)h * g.T + t] = (mm + log2f(sum)) * 0.6931471805599453f;
+    for (int k = 1; k < kTeams<D>; k++) {
+      const float* buf = sm + (k - 1) * kPart;
+      const float m1 = buf[kMl + (2 * i) * kTeam + team_tid<kTeam>()];
+      const float mm = fmaxf(m[i], m1), f0 = exp2f(m[i] - mm), f1 = exp2f(m1 - mm);
+      l[i] = l[i] * f0 + buf[kMl + (2 * i + 1) * kTeam + team_tid<kTeam>()] * f1;
+      m[i] = mm;
+#pragma unroll
+      for (int c = 0; c < D / 16; c++) acc[i][c] = acc[i][c] * f0 + got_acc<D>(buf, i, c) * f1;
+    }
+    store_row<T, D>(view_at<T>(a.o, 0, h, t), acc[i], 1.f / l[i]);
+    if (a.lse && tx == 0) a.lse[(int64_t)h * g.T + t] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
   }
 }
 
@@ -153,12 +162,12 @@ template <int D>
 constexpr int bwd_team() { return 2 * kTile * (D + 4) + kRows * kPitchP; }  // a tile of two operands, P or dS
 template <int D>
 constexpr int bwd_smem() {
-  return (2 * kRows * (D + 4) + 2 * bwd_team<D>()) * 4;  // two operands of the CTA's rows, and the teams' tiles
+  return (2 * kRows * (D + 4) + kTeams<D> * bwd_team<D>()) * 4;  // two operands of the CTA's rows, and the teams' tiles
 }
 
 // dS = P (dO V^T - delta), dQ += dS K
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, PackedBwdArgs a) {
+__global__ void __launch_bounds__(kThreads<D>) packed_dq_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
   float *Qs = sm, *Gs = Qs + kRows * P, *Ks = Gs + kRows * P + team() * bwd_team<D>(), *Vs = Ks + kTile * P,
@@ -170,8 +179,8 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
   const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
   const int nrow = min(kRows, end - row0);
-  load_rows<kThreads, T, D, kRows>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
-  load_rows<kThreads, T, D, kRows>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
+  load_rows<kThreads<D>, T, D, kRows>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<kThreads<D>, T, D, kRows>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
   float lse2[4], del[4], acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
   }
   __syncthreads();
   const int stop = row0 + nrow;
-  for (int k0 = start + team() * kTile; k0 < stop; k0 += 2 * kTile) {
+  for (int k0 = start + team() * kTile; k0 < stop; k0 += kTeams<D> * kTile) {
     const int nk = min(kTile, stop - k0);
     team_sync();
     load_rows<kTeam, T, D, kTile>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
@@ -222,20 +231,22 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedGeo g, P
     __syncwarp();
   }
   __syncthreads();
-  if (team() == 1) put_acc<D>(sm, acc);
+  if (team() > 0) put_acc<D>(sm + (team() - 1) * kRows * D, acc);
   __syncthreads();
-  if (team() == 1) return;
+  if (team() > 0) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
 #pragma unroll
-    for (int c = 0; c < D / 16; c++) acc[i][c] += got_acc<D>(sm, i, c);
+    for (int k = 0; k < kTeams<D> - 1; k++)
+#pragma unroll
+      for (int c = 0; c < D / 16; c++) acc[i][c] += got_acc<D>(sm + k * kRows * D, i, c);
     if (row0 + 4 * ty + i < end) store_row<T, D>(view_at<T>(a.dq, 0, h, row0 + 4 * ty + i), acc[i], scale);
   }
 }
 
 // rows = keys, columns = queries: dV += P^T dO, dK += dS^T Q over the rows of the group's heads
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g, PackedBwdArgs a) {
+__global__ void __launch_bounds__(kThreads<D>) packed_dkdv_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
   float *Ks = sm, *Vs = Ks + kRows * P, *Qs = Vs + kRows * P + team() * bwd_team<D>(), *Gs = Qs + kTile * P,
@@ -247,8 +258,8 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g,
   const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
   const int nk = min(kRows, end - key0);
-  load_rows<kThreads, T, D, kRows>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
-  load_rows<kThreads, T, D, kRows>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
+  load_rows<kThreads<D>, T, D, kRows>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
+  load_rows<kThreads<D>, T, D, kRows>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
   __syncthreads();
   float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
@@ -256,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g,
 #pragma unroll
     for (int c = 0; c < D / 16; c++) dk[i][c] = dv[i][c] = 0.f;
   const int nq_tiles = (end - key0 + kTile - 1) / kTile, steps = nq_tiles * g.G;
-  for (int step = team(); step < steps; step += 2) {
+  for (int step = team(); step < steps; step += kTeams<D>) {
     const int h = hk * g.G + step / nq_tiles, q0 = key0 + step % nq_tiles * kTile;
     const int nq = min(kTile, end - q0);
     team_sync();
@@ -286,19 +297,21 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedGeo g,
     __syncwarp();
   }
   __syncthreads();
-  if (team() == 1) {
-    put_acc<D>(sm, dk);
-    put_acc<D>(sm + kRows * D, dv);
+  if (team() > 0) {
+    put_acc<D>(sm + (2 * team() - 2) * kRows * D, dk);
+    put_acc<D>(sm + (2 * team() - 1) * kRows * D, dv);
   }
   __syncthreads();
-  if (team() == 1) return;
+  if (team() > 0) return;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
 #pragma unroll
-    for (int c = 0; c < D / 16; c++) {
-      dk[i][c] += got_acc<D>(sm, i, c);
-      dv[i][c] += got_acc<D>(sm + kRows * D, i, c);
-    }
+    for (int k = 0; k < kTeams<D> - 1; k++)
+#pragma unroll
+      for (int c = 0; c < D / 16; c++) {
+        dk[i][c] += got_acc<D>(sm + 2 * k * kRows * D, i, c);
+        dv[i][c] += got_acc<D>(sm + (2 * k + 1) * kRows * D, i, c);
+      }
     if (4 * ty + i >= nk) continue;
     store_row<T, D>(view_at<T>(a.dk, 0, hk, key0 + 4 * ty + i), dk[i], scale);
     store_row<T, D>(view_at<T>(a.dv, 0, hk, key0 + 4 * ty + i), dv[i], 1.f);
@@ -318,17 +331,17 @@ cudaError_t launch(K kern, int64_t blocks, int threads, int smem, const PackedGe
 template <typename T, int D>
 cudaError_t launch_bwd(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
   const cudaError_t e =
-      launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads, bwd_smem<D>(), g, a, st);
+      launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads<D>, bwd_smem<D>(), g, a, st);
   if (e != cudaSuccess) return e;
-  return launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads, bwd_smem<D>(), g, a, st);
+  return launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads<D>, bwd_smem<D>(), g, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_packed_fwd_simt(const PackedGeo& g, const PackedFwdArgs& a, cudaStream_t st) {
   const int64_t blocks = packed_list_cap(g, kListFwd) * g.Hq;
-  return g.d == 64 ? launch(packed_fwd_simt_kernel<float, 64>, blocks, kThreads, fwd_smem<64>(), g, a, st)
-                   : launch(packed_fwd_simt_kernel<float, 128>, blocks, kThreads, fwd_smem<128>(), g, a, st);
+  return g.d == 64 ? launch(packed_fwd_simt_kernel<float, 64>, blocks, kThreads<64>, fwd_smem<64>(), g, a, st)
+                   : launch(packed_fwd_simt_kernel<float, 128>, blocks, kThreads<128>, fwd_smem<128>(), g, a, st);
 }
 
 cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
