@@ -82,6 +82,8 @@ CASES = [
     ([800, 10], 0, 61, 7, 1, 64, BF16, "roots", "nhd"),     # 427 rows
     ([2000, 33, 1], 0, 40, 6, 2, 128, F32, "random", "nhd"),
     ([31] * 200, 1, 4, 8, 2, 64, BF16, "random", "hnd"),    # more segments than CTAs
+    ([1900, 40, 0, 700, 3000] * 20, 9, 5, 8, 4, 128, BF16, "absent", "nhd"),  # more segments than cuts, long and short
+    ([500, 40, 0, 700] * 40, 9, 3, 8, 4, 64, F32, "random", "hnd"),
     ([20000], 100, 2, 1, 1, 64, BF16, "chain", "hnd"),      # one segment over every CTA
 ]
 IDS = ["x".join(map(str, c[0][:6])) + "-" + "-".join(map(str, c[1:])) for c in CASES]
