@@ -25,6 +25,9 @@
 //   delta + sum_k P (dP - delta) = sum_k P dP up to the rounding of the difference alone,
 // and writes it back for the dK/dV kernel, which therefore runs second. Rows with more keys keep dO . O: their
 // O is an average, and its rounding small against dP.
+// Measured (8192 tokens, 16 heads of 128): dQ 0.32 ms, 2430 cycles a step, tensor pipe 63 % busy; dK/dV 0.39 ms,
+// 2850 cycles a step, tensor pipe 72 % busy, with shared memory (256 KB a step, 2048 cycles) close behind. 32K
+// tokens: 6.62 ms in a burst, 1340 TFLOP/s executed; 7.7 ms over a second, at the power cap.
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"
@@ -38,7 +41,8 @@ using namespace tc;
 
 constexpr int kSoftmax = 16;                    // softmax warps
 constexpr int kThreads = (kSoftmax + 4) * 32;
-// of 16 exponentials, on the FMA pipe: dK/dV and dQ kernel
+// of 16 pairs of exponentials, on the FMA pipe: dK/dV kernel (none: 3 % slower) and dQ kernel (2 and more: 2 to
+// 3 % slower over a second of calls)
 constexpr int kFma = 6, kFmaQ = 0;
 
 // zero the rows valid .. 127 of a 128-row operand tile (64-element halves of 128 rows x 128 bytes); one warp

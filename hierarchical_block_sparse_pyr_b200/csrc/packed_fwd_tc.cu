@@ -15,6 +15,9 @@
 // S(t + 1), O is at rest and may be rescaled without a wait.
 // A row sees 128 scores: the maximum comes first over all of them (so that the first half's P V may start
 // while the second half's exponentials run), O is rescaled only if the maximum grew by more than 2^8.
+// Measured (heads of 128): 24001 + 6000 + 2500 + 267 tokens, 16 heads: 1.95 ms in a burst, 1300 TFLOP/s, 78 % of
+// the measured peak; 2.3 ms over a second of calls, at the power cap. 8192 tokens: 211 us, tensor pipe 67 % busy,
+// about 2990 cycles a step of which 2048 are the products'.
 // Rows of V behind the sequence's end belong to others and may hold anything (0 * NaN is NaN): the P V
 // warp zeroes them in shared memory. Rows of K there only reach scores that the causal mask drops, rows of
 // Q only outputs that are not stored.

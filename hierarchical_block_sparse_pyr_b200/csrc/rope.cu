@@ -6,6 +6,8 @@
 // product of the position and the pair's turns per position in double (at position 10^6 a product in single
 // precision would be off by 2^-24 * 10^6 radians), reduced to a fraction of a turn in [-1/2, 1/2], and only
 // that fraction goes to single precision.
+// Measured: 32K tokens, 32 heads of 128, bf16: 81.8 us, 6.56 TB/s (the copy rate); 8194 tokens, 40 heads of 64 of
+// which half rotates, fp32, token-major: 29 us, 5.8 TB/s.
 #include <math.h>
 
 #include "view.cuh"

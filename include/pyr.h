@@ -19,7 +19,9 @@
  *     softmax accumulators and writes the output and the log-sum-exp.
  *
  * Conventions shared by every entry point
- *   Layouts (row-major, contiguous, every base pointer 16-byte aligned):
+ *   Layouts (row-major, contiguous, every base pointer 16-byte aligned; the
+ *   entry points that take a pyr_view take strided tensors instead, and state
+ *   their own shapes and limits):
  *     Q, O  [B][Hq][Nq][d]     K, V  [B][Hkv][N][d]
  *     pyr   [B][Hkv][P][2][d] bf16, level-major (level 0 first; node m of
  *           level l covers key blocks [m 2^l, min((m+1) 2^l, nb))). Each node
