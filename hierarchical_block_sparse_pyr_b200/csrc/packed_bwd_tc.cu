@@ -1,7 +1,7 @@
 // Gradients of packed-prompt attention on the tcgen05 tensor cores: bf16 operands, fp32 accumulation; P and
 // dS are rounded to bf16 for the products that read them. Two kernels, so that every gradient is summed by
-// one CTA in a fixed order (no atomics): S and dP are computed twice, 7 products of 128 x 128 x D where a
-// single pass with atomic sums of dQ would need 5.
+// one CTA in a fixed order (no atomics): S and dP are computed twice, and P K besides, 8 products of 128 x 128 x D
+// where a single pass with atomic sums of dQ would need 5, or 6 with P K.
 //
 // dK/dV: a CTA owns 128 keys of a key/value head and walks the 128-row query tiles from its own to the
 //   sequence's end, over the heads of the group:
@@ -11,23 +11,25 @@
 //   Tensor memory is full: S^T 128 columns, dP^T 128, dV D, dK D; P^T and dS^T overwrite their sources as
 //   bf16. While the softmax works on P^T(t), the tensor cores run dP^T(t) and dK(t - 1).
 // dQ: a CTA owns 128 queries of a head and walks the key tiles up to the diagonal:
-//     S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K
-//   with two S buffers (dS goes over S), one of dP, and dQ.
+//     S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K, PK += P K
+//   Tensor memory is full: S (P goes over it as bf16) 128 columns, dP (dS goes over it) 128, dQ D, PK D.
 // Both: persistent CTAs over the plan's lists (longest first, back and forth over the CTAs).
 //   warps 0-15  softmax: warpgroup w takes the columns 32 w .. 32 w + 31 of every row; its bf16 results go to
 //               columns 32 w .. 32 w + 15 of the buffer, so that no warpgroup touches another's columns. Four
 //               warps a scheduler: with two, the waits and tensor-memory loads of a step were not covered
-//   warp 16     TMA      warp 17  products (S and dQ in the dQ kernel)      warp 18  dP in the dQ kernel
-//   warp 19     lse, delta and tails (dK/dV only)
-// delta = dO . O is taken from the rounded O. Where a row sees few keys, dP and delta nearly cancel (with one
-// key they are equal), and that rounding would be what is left. The rows of a sequence's first tile see one
-// key tile, so the dQ kernel has all of their P and dP at hand: it refines delta by one step,
-//   delta + sum_k P (dP - delta) = sum_k P dP up to the rounding of the difference alone,
-// and writes it back for the dK/dV kernel, which therefore runs second. Rows with more keys keep dO . O: their
-// O is an average, and its rounding small against dP.
-// Measured (8192 tokens, 16 heads of 128): dQ 0.32 ms, 2430 cycles a step, tensor pipe 63 % busy; dK/dV 0.39 ms,
-// 2850 cycles a step, tensor pipe 72 % busy, with shared memory (256 KB a step, 2048 cycles) close behind. 32K
-// tokens: 6.62 ms in a burst, 1340 TFLOP/s executed; 7.7 ms over a second, at the power cap.
+//   warp 16     TMA      warp 17  products      warp 19  lse, delta and tails (dK/dV only)
+// delta = dO . O comes from the rounded O and is off by about 2^-9 |(dO_i O_i)_i|. The rounding of dS is small
+// against |dP - delta|, that error only against |O|, and the two have nothing to do with each other: values with a
+// component in common, peaked scores or few keys in a row make the error the larger one (values and keys with a
+// common component of 4 and 2 times their spread: dQ 13 % off). The dQ kernel has all of a row's P and dP, and
+//   rest = sum_k P (dP - delta)   makes   delta + rest = sum_k P dP   up to the rounding of the differences alone,
+// so it subtracts rest PK from dQ, and writes delta + rest back for the dK/dV kernel, which therefore runs second.
+// The rows of a sequence's first tile see one key tile: they get delta + rest before dS is formed, which leaves
+// exactly 0 where a row sees one key. (8192 tokens, 16 heads: without PK and rest 764 us for all of the gradients,
+// with them 830; sustained 32K tokens 7.7 and 8.5 ms.)
+// Measured (8192 tokens, 16 heads of 128): dK/dV 0.39 ms, 2850 cycles a step, tensor pipe 72 % busy, with shared
+// memory (256 KB a step, 2048 cycles) close behind; dQ 0.39 ms, where the softmax warps' chain of loads,
+// exponentials and stores is the bound, 2900 cycles a step against 2048 of products.
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"
@@ -41,9 +43,8 @@ using namespace tc;
 
 constexpr int kSoftmax = 16;                    // softmax warps
 constexpr int kThreads = (kSoftmax + 4) * 32;
-// of 16 pairs of exponentials, on the FMA pipe: dK/dV kernel (none: 3 % slower) and dQ kernel (2 and more: 2 to
-// 3 % slower over a second of calls)
-constexpr int kFma = 6, kFmaQ = 0;
+// of 16 pairs of exponentials, on the FMA pipe (dK/dV kernel: none 3 % slower; dQ kernel: none 8 % slower, 4 pairs 1 %)
+constexpr int kFma = 6;
 
 // zero the rows valid .. 127 of a 128-row operand tile (64-element halves of 128 rows x 128 bytes); one warp
 template <int D>
@@ -453,9 +454,9 @@ struct QPlan {
   static constexpr int TB = 128 * D * 2;
   static constexpr int NK = 3, NV = 2;  // K stages (a K tile lives until dQ has read it), V stages
   static constexpr int kQ = 0, kG = TB, kK = 2 * TB, kV = kK + NK * TB;
-  static constexpr int kSum = kV + NV * TB;  // [128] fp32: row sums on their way through the warpgroups
-  static constexpr int kBar = kSum + 512;
-  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 1 + 1 + 1 + 1 + 2 + 16;
+  static constexpr int kSum = kV + NV * TB;  // [2][128] fp32: row sums on their way through the warpgroups
+  static constexpr int kBar = kSum + 1024;
+  static constexpr int kNumBars = 2 + 2 * NK + 2 * NV + 2 + 2 + 2 + 1 + 16;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kBytes = kMisc + 16 + 1024;
 };
@@ -488,19 +489,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = smem_align<1024>(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PL::kBar);
   uint64_t* bar_q_full = bars;      // Q and dO of the item
-  uint64_t* bar_q_free = bars + 1;  // both issuers have read them
+  uint64_t* bar_q_free = bars + 1;  // its last S and dP have read them
   uint64_t* bar_k_full = bars + 2;
   uint64_t* bar_k_free = bar_k_full + NK;
   uint64_t* bar_v_full = bar_k_free + NK;
   uint64_t* bar_v_free = bar_v_full + NV;
-  uint64_t* bar_s_full = bar_v_free + NV;   // [2]
-  uint64_t* bar_ds_full = bar_s_full + 2;   // [2]
-  uint64_t* bar_dp_full = bar_ds_full + 2;
-  uint64_t* bar_dp_free = bar_dp_full + 1;
-  uint64_t* bar_acc_full = bar_dp_free + 1;
+  uint64_t* bar_s_full = bar_v_free + NV;
+  uint64_t* bar_p_full = bar_s_full + 1;    // P stands where S was
+  uint64_t* bar_dp_full = bar_p_full + 1;
+  uint64_t* bar_ds_full = bar_dp_full + 1;  // dS stands where dP was
+  uint64_t* bar_acc_full = bar_ds_full + 1;
   uint64_t* bar_acc_free = bar_acc_full + 1;
-  uint64_t* bar_drain = bar_acc_free + 1;  // [2]
-  uint64_t* bar_sum = bar_drain + 2;       // [4][4] rows, warpgroup: has added its part
+  uint64_t* bar_drain = bar_acc_free + 1;
+  uint64_t* bar_sum = bar_drain + 1;  // [4][4] rows, warpgroup: has added its part
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + PL::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + PL::kMisc + 4);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&tmV);
     tma_prefetch_map(&tmG);
     mbar_init(bar_q_full, 1);
-    mbar_init(bar_q_free, 2);
+    mbar_init(bar_q_free, 1);
     for (int s = 0; s < NK; s++) {
       mbar_init(bar_k_full + s, 1);
       mbar_init(bar_k_free + s, 1);
@@ -520,16 +521,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_v_full + s, 1);
       mbar_init(bar_v_free + s, 1);
     }
-    for (int i = 0; i < 2; i++) {
-      mbar_init(bar_s_full + i, 1);
-      mbar_init(bar_ds_full + i, kSoftmax);
-      mbar_init(bar_drain + i, 1);
-    }
-    for (int i = 0; i < 16; i++) mbar_init(bar_sum + i, 1);
+    mbar_init(bar_s_full, 1);
+    mbar_init(bar_p_full, kSoftmax);
     mbar_init(bar_dp_full, 1);
-    mbar_init(bar_dp_free, kSoftmax);
+    mbar_init(bar_ds_full, kSoftmax);
     mbar_init(bar_acc_full, 1);
     mbar_init(bar_acc_free, kSoftmax);
+    mbar_init(bar_drain, 1);
+    for (int i = 0; i < 16; i++) mbar_init(bar_sum + i, 1);
     fence_mbar_init();
     *abort_flag = 0;
   }
@@ -541,8 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tS = tmem, tP = tmem + 256, tDQ = tmem + 384;  // S[b] at 128 b
-  const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024);
+  const uint32_t tS = tmem, tP = tmem + 128, tDQ = tmem + 256, tPK = tmem + 256 + D;
   QItem it;
   const int tiles = uniform(packed_tiles(g, a.plan, kListQ, a.status));
 
@@ -579,18 +577,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kSoftmax + 1) {
     regs_dec<64>();
-    // ------------------------------------------------------------ S and dQ
-    // S runs two steps ahead of dQ, over the ends of the items: S(u + 2) goes over dS(u) behind dQ(u), as
-    // products of one thread run in the order of issue.
-    const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024);
+    // ------------------------------------------------------------ all products: P K(u) and S(u + 1) while the
+    // softmax works on dS(u), dQ(u) and dP(u + 1) while it works on P(u + 1). S(u + 1) goes over P(u) and dP(u + 1)
+    // over dS(u) behind the products that read them, as products of one thread run in the order of issue. At an
+    // item's end S(u + 1) comes behind dQ(u), which would otherwise wait for the next item's Q.
+    const uint64_t dQ = sdesc_sw128(smem_u32(smem + PL::kQ), 16, 1024), dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
+    const uint64_t dK = sdesc_sw128(smem_u32(smem + PL::kK), 16, 1024), dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
     const uint64_t dKm = sdesc_sw128(smem_u32(smem + PL::kK), 16384, 1024);
-    bool ok = true;
-    int us = 0, si = 0, sr = 0, sitems = 0;  // next S: step, step of its item, item
+    bool ok = true, last = false;
+    int us = 0, si = 0, sr = 0, sitems = 0;  // next S: step, step of its item, its item in the list and here
     QItem is;
     bool more = q_item(g, a.plan, tiles, list_at(0), &is);
     auto scores = [&]() {
       if (!more || !ok) return;
-      const int s = us % NK, b = us & 1;
+      const int s = us % NK;
       if (si == 0) ok = warp_wait(bar_q_full, sitems & 1, abort_flag);
       if (ok) ok = warp_wait(bar_k_full + s, (us / NK) & 1, abort_flag);
       if (!ok) return;
@@ -603,66 +603,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       if (elect_one()) {
-        mma_nt<D>(tS + b * 128, dQ, dK + (uint64_t)(s * (TB >> 4)));
-        umma_commit(bar_s_full + b);
-        if (si == is.steps - 1) umma_commit(bar_q_free);
+        mma_nt<D>(tS, dQ, dK + (uint64_t)(s * (TB >> 4)));
+        umma_commit(bar_s_full);
       }
       __syncwarp();
       us++;
-      if (++si == is.steps) {
+      last = ++si == is.steps;
+      if (last) {
         si = 0;
         sitems++;
         more = q_item(g, a.plan, tiles, list_at(++sr), &is);
       }
     };
+    auto dprob = [&](int v) {  // of the step whose S was the last to be issued
+      if (!ok || us <= v) return;
+      const int s = v % NV;
+      ok = warp_wait(bar_v_full + s, (v / NV) & 1, abort_flag);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_nt<D>(tP, dG, dV + (uint64_t)(s * (TB >> 4)));
+        umma_commit(bar_dp_full);
+        umma_commit(bar_v_free + s);
+        if (last) umma_commit(bar_q_free);
+      }
+      __syncwarp();
+    };
     scores();
-    scores();
+    dprob(0);
     int items = 0, u = 0;
     for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       for (int i = 0; i < it.steps && ok; i++, u++) {
-        const int b = u & 1, s = u % NK;
-        ok = warp_wait(bar_ds_full + b, (u >> 1) & 1, abort_flag);
+        const int s = u % NK;
+        const uint64_t at = (uint64_t)(s * (TB >> 4));
+        ok = warp_wait(bar_p_full, u & 1, abort_flag);
         if (ok && i == 0 && items > 0) ok = warp_wait(bar_acc_free, (items - 1) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {
-          mma_acc<D, 0, 8>(tDQ, tS + b * 128, dKm + (uint64_t)(s * (TB >> 4)), i > 0);
-          if (i == it.steps - 1) umma_commit(bar_acc_full);
+        if (it.steps > 1) {
+          if (elect_one()) mma_acc<D, 0, 8>(tPK, tS, dKm + at, i > 0);
+          __syncwarp();
         }
-        __syncwarp();
-        // (K(u + 2) is in flight or there: only K(u + 3) needs the stage of K(u))
-        scores();
-        if (ok && elect_one()) umma_commit(bar_k_free + s);
-        __syncwarp();
-      }
-    }
-    drain(bar_drain);
-  } else if (warp == kSoftmax + 2) {
-    regs_dec<64>();
-    // ------------------------------------------------------------ dP
-    const uint64_t dG = sdesc_sw128(smem_u32(smem + PL::kG), 16, 1024);
-    const uint64_t dV = sdesc_sw128(smem_u32(smem + PL::kV), 16, 1024);
-    bool ok = true;
-    int items = 0, u = 0;
-    for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
-      ok = warp_wait(bar_q_full, items & 1, abort_flag);
-      for (int i = 0; i < it.steps && ok; i++, u++) {
-        const int s = u % NV;
-        ok = warp_wait(bar_v_full + s, (u / NV) & 1, abort_flag);
-        if (ok && u > 0) ok = warp_wait(bar_dp_free, (u - 1) & 1, abort_flag);
+        if (i + 1 < it.steps) scores();
+        if (ok) ok = warp_wait(bar_ds_full, u & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_nt<D>(tP, dG, dV + (uint64_t)(s * (TB >> 4)));
-          umma_commit(bar_dp_full);
-          umma_commit(bar_v_free + s);
-          if (i == it.steps - 1) umma_commit(bar_q_free);
+          mma_acc<D, 0, 8>(tDQ, tP, dKm + at, i > 0);
+          umma_commit(bar_k_free + s);
+          if (i == it.steps - 1) umma_commit(bar_acc_full);
         }
         __syncwarp();
+        if (i + 1 == it.steps) scores();
+        dprob(u + 1);
       }
     }
-    drain(bar_drain + 1);
-  } else if (warp == kSoftmax + 3) {
+    drain(bar_drain);
+  } else if (warp >= kSoftmax + 2) {
     regs_dec<64>();
   } else {
     // ------------------------------------------------------------ softmax
@@ -672,31 +669,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
     const int rr = wq * 32 + lane;
     bool ok = true;
-    volatile float* sum = reinterpret_cast<volatile float*>(smem + PL::kSum) + rr;
     int items = 0, u = 0, sums = 0;  // sums: rounds of the row sums so far
+    // A row's sum over its four warpgroups' parts, added in their order. Two buffers: a warpgroup that is a round
+    // ahead writes into the other one, and cannot be two ahead, as every round waits for all four.
+    auto row_sum = [&](float part) {
+      volatile float* sum = reinterpret_cast<volatile float*>(smem + PL::kSum) + (sums & 1) * 128 + rr;
+      if (wg > 0) {
+        ok = warp_wait(bar_sum + 4 * wq + wg - 1, sums & 1, abort_flag);
+        part += *sum;
+      }
+      *sum = part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_sum + 4 * wq + wg);
+      if (ok) ok = warp_wait(bar_sum + 4 * wq + 3, sums & 1, abort_flag);
+      sums++;
+      return *sum;
+    };
     for (int r = 0; ok && q_item(g, a.plan, tiles, list_at(r), &it); r++, items++) {
       const int row = it.row0 + rr;
       const bool live = it.row0 + wq * 32 < it.end;
       const int64_t at = (int64_t)it.head * g.T + min(row, it.end - 1);
       const float nl = -kLog2e * a.lse[at], nd = -a.delta[at];
       const float2 scl = make_float2(sl2, sl2), off = make_float2(nl, nl);
-      float2 del = make_float2(nd, nd);
+      float2 del = make_float2(nd, nd), rest = make_float2(0.f, 0.f);
       for (int i = 0; i < it.steps; i++, u++) {
-        const int b = u & 1;
         const bool diag = i == it.steps - 1;
-        ok = warp_wait(bar_s_full + b, (u >> 1) & 1, abort_flag);
+        ok = warp_wait(bar_s_full, u & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         float p[32];
         if (live) {
-          tmem_ld32(tS + b * 128 + base, p);
+          uint32_t pk[16];
+          tmem_ld32(tS + base, p);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 16; c++) {
-            const float2 x = exp2_mix<16, kFmaQ, 3>(c, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
+            const float2 x = exp2_mix<16, kFma, 3>(c, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
             p[2 * c] = x.x, p[2 * c + 1] = x.y;
           }
+          if (diag) {
+#pragma unroll
+            for (int c = 0; c < 32; c++) p[c] = wg * 32 + c <= rr ? p[c] : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 16; c++) pk[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+          tmem_st16u(tS + base, pk);
+          tmem_wait_st();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p_full);
         ok = warp_wait(bar_dp_full, u & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -706,28 +728,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tP + base, d);
           tmem_wait_ld();
           if (diag) {
-            // columns behind the row hold what must not be summed, or another sequence's values
+            // columns behind the row may hold another sequence's values
 #pragma unroll
-            for (int c = 0; c < 32; c++) {
-              p[c] = wg * 32 + c <= rr ? p[c] : 0.f;
-              d[c] = wg * 32 + c <= rr ? d[c] : 0.f;
-            }
+            for (int c = 0; c < 32; c++) d[c] = wg * 32 + c <= rr ? d[c] : 0.f;
           }
-          if (it.steps == 1) {
-            // this tile is all that the row sees: delta += sum_k P (dP - delta), the warpgroups in order
+          if (it.steps == 1) {  // all that the row sees
             float part = 0.f;
 #pragma unroll
             for (int c = 0; c < 32; c++) part = fmaf(p[c], d[c] + nd, part);
-            if (wg > 0) {
-              ok = warp_wait(bar_sum + 4 * wq + wg - 1, sums & 1, abort_flag);
-              part += *sum;
-            }
-            *sum = part;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_sum + 4 * wq + wg);
-            if (ok) ok = warp_wait(bar_sum + 4 * wq + 3, sums & 1, abort_flag);
-            sums++;
-            const float refined = -nd + *sum;
+            const float refined = -nd + row_sum(part);
             del = make_float2(-refined, -refined);
             if (wg == 0 && row < it.end) a.delta[at] = refined;
           }
@@ -735,26 +744,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 16; c++) {
             const float2 x =
                 __fmul2_rn(make_float2(p[2 * c], p[2 * c + 1]), __fadd2_rn(make_float2(d[2 * c], d[2 * c + 1]), del));
+            rest = __fadd2_rn(rest, x);
             pk[c] = pack_bf16(x.x, x.y);
           }
-          tmem_st16u(tS + b * 128 + base, pk);
+          tmem_st16u(tP + base, pk);
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
         if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive(bar_dp_free);
-          mbar_arrive(bar_ds_full + b);
-        }
+        if (lane == 0) mbar_arrive(bar_ds_full);
       }
       if (!ok) break;
       // ---- epilogue: 32 columns a warpgroup ----
+      float c = 0.f;
+      if (live && it.steps > 1) {
+        c = row_sum(rest.x + rest.y);
+        if (wg == 0 && row < it.end) a.delta[at] = -nd + c;  // for the dK/dV kernel
+        if (!ok) break;
+      }
       ok = warp_wait(bar_acc_full, items & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
-      if (live && wg * 32 < D)
-        store_acc<32>(tDQ + base, view_at<__nv_bfloat16>(a.dq, 0, it.head, row) + wg * 32, scale, row < it.end);
+      if (live && wg * 32 < D) {
+        float o[32];
+        tmem_ld32(tDQ + base, o);
+        if (it.steps > 1) {
+          float k[32];
+          tmem_ld32(tPK + base, k);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e++) o[e] = fmaf(-c, k[e], o[e]);
+        } else {
+          tmem_wait_ld();
+        }
+        if (row < it.end) store32_bf16(view_at<__nv_bfloat16>(a.dq, 0, it.head, row) + wg * 32, o, scale);
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_acc_free);

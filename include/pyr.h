@@ -566,9 +566,11 @@ PYR_API int packed_forward(const packed_shape* s, const pyr_view* Q, const pyr_v
  *   dQ = sum_k dS k / sqrt(d), dK = sum_t dS q / sqrt(d), dV = sum_t P dO,
  * t running over the rows of all heads of the key's group.
  *   Q, K, V, O, dO views as above; O and lse as written by packed_forward.
- *   delta  device fp32 [Hq][T] workspace (overwritten with D; the rows of a
- *          sequence's first tile, whose few keys make dO . v and D cancel, get
- *          D as sum_k P (dO . v) instead of from the rounded O).
+ *   delta  device fp32 [Hq][T] workspace (overwritten with D). In bf16 D is
+ *          sum_k P (dO . v), formed as dO . O of the rounded O and the rest
+ *          that sum_k P (dO . v - D) leaves, for dQ as for dK: the rounding of
+ *          O does not reach the gradients. In fp32 it is dO . O, and that sum
+ *          for the rows of a sequence's first tile.
  *   dQ     view [Hq][T][d]; dK, dV views [Hkv][T][d] (written; no overlap with
  *          any other operand).
  * Every gradient element is summed by one thread block in a fixed order, in
