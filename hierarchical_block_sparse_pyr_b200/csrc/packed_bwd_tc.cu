@@ -375,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; e += 2) {
             const float4 nl = st[e / 2];
             const int o = 2 * e;
-            const float2 x = exp2_mix<16, kFma, 3>(e, __ffma2_rn(make_float2(p[o], p[o + 1]), scl, make_float2(nl.x, nl.y)));
+            const float2 x = exp2_mix<16, kFma, 3, true>(e, __ffma2_rn(make_float2(p[o], p[o + 1]), scl, make_float2(nl.x, nl.y)));
             const float2 y =
-                exp2_mix<16, kFma, 3>(e + 1, __ffma2_rn(make_float2(p[o + 2], p[o + 3]), scl, make_float2(nl.z, nl.w)));
+                exp2_mix<16, kFma, 3, true>(e + 1, __ffma2_rn(make_float2(p[o + 2], p[o + 3]), scl, make_float2(nl.z, nl.w)));
             p[o] = x.x, p[o + 1] = x.y, p[o + 2] = y.x, p[o + 3] = y.y;
           }
           if (diag) {
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 16; c++) {
-            const float2 x = exp2_mix<16, kFma, 3>(c, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
+            const float2 x = exp2_mix<16, kFma, 3, true>(c, __ffma2_rn(make_float2(p[2 * c], p[2 * c + 1]), scl, off));
             p[2 * c] = x.x, p[2 * c + 1] = x.y;
           }
           if (diag) {

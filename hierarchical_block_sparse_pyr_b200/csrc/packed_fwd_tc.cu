@@ -313,9 +313,10 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 128; c++) s[c] = c < lim ? s[c] : -INFINITY;
         }
-        const float mx = fmaxf(fmaxf(max32(s), max32(s + 32)), fmaxf(max32(s + 64), max32(s + 96)));
-        const float m_new = fmaxf(m_ref, mx * sl2);
-        const bool need = (m_ref != -INFINITY) && (m_new > m_ref + kRescale);
+        // a NaN score makes the row's maximum, and with it all that follows, NaN
+        const float mx = max_nan(max_nan(max32(s), max32(s + 32)), max_nan(max32(s + 64), max32(s + 96)));
+        const float m_new = max_nan(m_ref, mx * sl2);
+        const bool need = (m_ref != -INFINITY) && !(m_new <= m_ref + kRescale);
         float factor = 1.f;
         if (need) {
           factor = ex2(m_ref - m_new);
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(FPlan<D>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; c++) {
             const float2 x = __ffma2_rn(make_float2(s[half * 64 + 2 * c], s[half * 64 + 2 * c + 1]), scl, off);
-            const float2 e = exp2_mix<32, kFma, 4>(c, x);
+            const float2 e = exp2_mix<32, kFma, 4, false>(c, x);
             acc[c & 3] = __fadd2_rn(acc[c & 3], e);
             pk[c] = pack_bf16(e.x, e.y);
           }

@@ -55,13 +55,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// maxima that are NaN if an operand is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float max32(const float* s) {
   float a[11];
 #pragma unroll
-  for (int k = 0; k < 10; k++) a[k] = fmax3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
-  a[10] = fmaxf(s[30], s[31]);
-  const float x = fmax3(a[0], a[1], a[2]), y = fmax3(a[3], a[4], a[5]), z = fmax3(a[6], a[7], a[8]);
-  return fmaxf(fmax3(x, y, z), fmaxf(a[9], a[10]));
+  for (int k = 0; k < 10; k++) a[k] = max3_nan(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
+  a[10] = max_nan(s[30], s[31]);
+  const float x = max3_nan(a[0], a[1], a[2]), y = max3_nan(a[3], a[4], a[5]), z = max3_nan(a[6], a[7], a[8]);
+  return max_nan(max3_nan(x, y, z), max_nan(a[9], a[10]));
 }
 
 // 16 consecutive 32-bit columns of this thread's lane, stored from registers.
@@ -79,12 +90,15 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* r) {
 // (adding 1.5 * 2^23 leaves n in the low bits) and f in [-1/2, 1/2]; 2^f is 1 + f (c1 + f (c2 + ...)) with
 // the coefficients of least maximum relative error for that form (found by linear programming on a grid of
 // 4001 points): 1.0e-4 for degree 3, 2.9e-6 for degree 4, against 2^-9 = 2e-3 of the rounding to bf16 that
-// follows. Below -127 the clamp makes n = -127, f = 0, and the exponent arithmetic gives exactly 0.
-template <int DEG>
+// follows. Below -127 the clamp makes n = -127, f = 0, and the exponent gives exactly 0.
+// KEEP_NAN: NaN stays NaN, as on the MUFU unit: the clamp hands it on, and 2^n is a factor instead of an addition to
+// the exponent's bits, which would make a number of it. Without, NaN becomes 0, for rows whose other columns are NaN
+// as well.
+template <int DEG, bool KEEP_NAN>
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
   constexpr float kMagic = 12582912.f;
-  x.x = fmaxf(x.x, -127.f);
-  x.y = fmaxf(x.y, -127.f);
+  x.x = KEEP_NAN ? max_nan(x.x, -127.f) : fmaxf(x.x, -127.f);
+  x.y = KEEP_NAN ? max_nan(x.y, -127.f) : fmaxf(x.y, -127.f);
   const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
   const float2 n = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
   const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
@@ -98,14 +112,17 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
     p = __ffma2_rn(f, p, make_float2(0.6931241f, 0.6931241f));
   }
   p = __ffma2_rn(f, p, make_float2(1.f, 1.f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+  if (!KEEP_NAN)
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+  return __fmul2_rn(p, make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
+                                   __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u)));
 }
 
 // 2^x of the c-th of N pairs: the last FMA of them on the FMA pipe, the others on MUFU
-template <int N, int FMA, int DEG>
+template <int N, int FMA, int DEG, bool KEEP_NAN>
 __device__ __forceinline__ float2 exp2_mix(int c, float2 x) {
-  if (c >= N - FMA) return exp2_fma<DEG>(x);
+  if (c >= N - FMA) return exp2_fma<DEG, KEEP_NAN>(x);
   return make_float2(ex2(x.x), ex2(x.y));
 }
 

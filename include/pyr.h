@@ -521,7 +521,9 @@ PYR_API int rope_apply(const rope_spec* spec, int B, int Hq, int Hkv, int N, int
  * tokens of its sequence, with softmax scale 1/sqrt(d). Sequences may be
  * empty. Tokens outside every sequence (before cu[0], or behind cu[S]) belong
  * to the caller: nothing of them is used and their outputs are left as they
- * were. The values inside the sequences are taken to be finite.
+ * were. A NaN inside a sequence reaches every output and every gradient that
+ * depends on it, and may reach others of its sequence. Infinities are not
+ * provided for.
  */
 typedef struct packed_shape {
   int S;     /* sequences, >= 1 */

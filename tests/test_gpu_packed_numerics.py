@@ -1,4 +1,4 @@
-"""Packed prompts in bf16 where the gradients' terms cancel.
+"""Packed prompts in bf16 where the gradients' terms cancel, and with values that are not finite.
 
 The error model of the gradients. Inputs are exact; with u = 2^-8 / sqrt(3), the largest root mean square of a
 rounding to bf16 relative to the value, and independent roundings:
@@ -104,3 +104,51 @@ def test_gradients_where_terms_cancel(kind, lens, Hq, Hkv, d):
         for part, rows in (("up to row 127", at < 128), ("behind", at >= 128)):
             e, bound = (got.double() - w)[:, rows].norm(), 1.25 * s[:, rows].sum().sqrt()
             assert float(e) <= float(bound), (name, part, float(e), float(bound), float(w[:, rows].norm()))
+
+
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF16, 128, 4, 2), (BF16, 64, 3, 3), (F32, 64, 2, 1)])
+def test_a_key_that_is_not_a_number(dtype, d, Hq, Hkv):
+    """Every position of a NaN among 130 keys, one sequence each, between sequences of numbers: it reaches every
+    output and every gradient that depends on it, whatever the position, and no other sequence."""
+    L = 130
+    lens = [L, 20] * L
+    cu, Q, K, V, dO = _make(lens, Hq, Hkv, d, dtype, 7)
+    Q, K, V, dO = (x.to(dtype) for x in (Q, K, V, dO))
+    want = _train(cu, Q, K, V, dO)
+    K = K.clone()
+    for j in range(L):
+        K[:, cu[2 * j] + j] = float("nan")
+    O, lse, (dQ, dK, dV) = _train(cu, Q, K, V, dO)
+    for j in range(L):
+        a, b = cu[2 * j], cu[2 * j + 1]
+        assert torch.equal(O[:, a:a + j], want[0][:, a:a + j]) and torch.equal(lse[:, a:a + j], want[1][:, a:a + j]), j
+        assert O[:, a + j:b].isnan().all() and lse[:, a + j:b].isnan().all(), j
+        assert dQ[:, a + j:b].isnan().all() and dK[:, a:b].isnan().all() and dV[:, a:b].isnan().all(), j
+    clean = torch.cat([torch.arange(cu[i], cu[i + 1]) for i in range(1, 2 * L, 2)]).cuda()
+    assert torch.equal(O[:, clean], want[0][:, clean]) and torch.equal(lse[:, clean], want[1][:, clean])
+    for x, y in zip((dQ, dK, dV), want[2]):
+        assert torch.equal(x[:, clean], y[:, clean])
+
+
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [(BF16, 128, 4, 2), (BF16, 64, 3, 3), (F32, 64, 2, 1)])
+def test_a_query_that_is_not_a_number(dtype, d, Hq, Hkv):
+    """The same for a NaN query: its output, its gradient and those of the keys and values that it sees."""
+    L = 130
+    lens = [L, 20] * L
+    cu, Q, K, V, dO = _make(lens, Hq, Hkv, d, dtype, 8)
+    Q, K, V, dO = (x.to(dtype) for x in (Q, K, V, dO))
+    want = _train(cu, Q, K, V, dO)
+    Q = Q.clone()
+    bad = torch.zeros(cu[-1], dtype=torch.bool, device="cuda")
+    for j in range(L):
+        bad[cu[2 * j] + j] = True
+    Q[:, bad] = float("nan")
+    O, lse, (dQ, dK, dV) = _train(cu, Q, K, V, dO)
+    assert O[:, bad].isnan().all() and lse[:, bad].isnan().all() and dQ[:, bad].isnan().all()
+    assert torch.equal(O[:, ~bad], want[0][:, ~bad]) and torch.equal(lse[:, ~bad], want[1][:, ~bad])
+    for j in range(L):
+        a = cu[2 * j]
+        assert dK[:, a:a + j + 1].isnan().all() and dV[:, a:a + j + 1].isnan().all(), j
+    clean = torch.cat([torch.arange(cu[i], cu[i + 1]) for i in range(1, 2 * L, 2)]).cuda()
+    for x, y in zip((dQ, dK, dV), want[2]):
+        assert torch.equal(x[:, clean], y[:, clean])
