@@ -460,6 +460,13 @@ def _call(fn, what, device, stream, *args):
         raise PyrError(rc, what)
 
 
+def _torch_stream(stream, device):
+    """A stream argument (None, a torch stream, a raw handle) as a torch stream or None, for allocations."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+
+
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
@@ -535,14 +542,14 @@ def _plan_words(s):
 
 def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
     """The work list of sequences [cu[i], cu[i+1]) (int32 CUDA tensor [S + 1]); it serves every packed_forward
-    and packed_backward of this shape and these boundaries. Returns plan (allocated if None)."""
+    and packed_backward of this shape and these boundaries. Returns plan (allocated if None, as memory of the
+    stream that writes it: another stream's user waits for that stream and keeps the plan until it is done)."""
     dev = _device_of(cu)
     c = _need(cu, "cu", torch.int32, s.S + 1, dev)
     n = packed_plan_elems(s)
     if plan is None:
-        plan = torch.empty(max(n, 1), dtype=torch.int32, device=cu.device)
-        if isinstance(stream, torch.cuda.Stream):
-            plan.record_stream(stream)
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            plan = torch.empty(max(n, 1), dtype=torch.int32, device=cu.device)
     _call(_L().packed_plan, "packed_plan", dev, stream, ctypes.byref(s), c,
           _need(plan, "plan", torch.int32, n, dev), _plain(status, "status", torch.int32, 1, dev))
     return plan
