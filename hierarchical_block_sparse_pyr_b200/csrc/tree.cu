@@ -42,7 +42,8 @@ struct Part<4> {
 
 // One warp a row: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of the row's segment in
 // stream order. Segments that one CTA held whole were written by it. blockIdx.x is a segment, or (where
-// there are more segments than cuts between CTAs) a cut: the first cut of a segment does its rows.
+// there are more segments than cuts between CTAs) a cut: the first cut of a segment does its rows. A sum of 0 is an
+// absent slot's; a NaN score's is NaN.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, TreeArgs a, bool by_cut) {
   extern __shared__ int s_pre[];
@@ -114,9 +115,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(TreeGeo g, T
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const int h = hk * g.G + hg;
-    acc.store(view_at<T>(a.o, b, h, t) + lane * E, l > 0.f ? 1.f / l : 0.f);
+    acc.store(view_at<T>(a.o, b, h, t) + lane * E, l != 0.f ? 1.f / l : 0.f);
     if (a.lse && lane == 0)
-      a.lse[((int64_t)b * g.Hq + h) * g.T + t] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      a.lse[((int64_t)b * g.Hq + h) * g.T + t] = l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 }
 

@@ -91,10 +91,10 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
       }
       if (whole) {
         const int h = hk * g.G + (r0 + r) / g.T, t = (r0 + r) % g.T;
-        store_row<T, D>(view_at<T>(a.o, b, h, t), acc[i], l[i] > 0.f ? 1.f / l[i] : 0.f);
+        store_row<T, D>(view_at<T>(a.o, b, h, t), acc[i], l[i] != 0.f ? 1.f / l[i] : 0.f);
         if (a.lse && tx == 0)
           a.lse[((int64_t)b * g.Hq + h) * g.T + t] =
-              l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
+              l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
       } else {
         store_row<float, D>(a.part_o + (part + r) * D, acc[i], 1.f);
         if (tx == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (part + r)) = make_float2(m[i], l[i]);

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t part =
           (int64_t)(blockIdx.x * 2 + pc->part) * g.RR + (SPLIT ? 0 : sl) * 128 + rt;
       if (whole) {
-        const float inv = l_sum > 0.f ? 1.f / l_sum : 0.f;
+        const float inv = l_sum != 0.f ? 1.f / l_sum : 0.f;  // 0: absent (a NaN score's sum is NaN)
         w0 *= inv;
         w1 *= inv;
       }
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row_ok && whole) {
         if (a.lse)
           a.lse[((int64_t)b * g.Hq + head) * g.T + tok] =
-              l_sum > 0.f ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
+              l_sum != 0.f ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
       } else if (row_ok) {
         *reinterpret_cast<float2*>(a.part_ml + 2 * part) = make_float2(m_ref, l_sum);
       }

@@ -619,7 +619,9 @@ PYR_API size_t tree_workspace_bytes(const tree_shape* s);
  *          lse = -inf, and the cache rows of absent slots are not used.
  *   workspace device, 16-byte aligned, >= tree_workspace_bytes bytes; calls
  *          that share one must be ordered on a stream.
- * Cache rows at or behind len[b] + T are not used. The cache is read once per
+ * Cache rows at or behind len[b] + T are not used. A NaN in a query or a key
+ * makes O and lse of the tokens that see it NaN; one in a value, or an infinity,
+ * may reach all tokens of its sequence. The cache is read once per
  * key/value head for up to 256 query rows (T tokens of Hq / Hkv heads); the
  * work is split evenly over the GPU along the cached tokens and the parts are
  * joined in a fixed order.
