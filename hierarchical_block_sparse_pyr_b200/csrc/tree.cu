@@ -138,7 +138,7 @@ int make_tree_geo(const tree_shape* s, TreeGeo* g) {
   if (!s || s->B <= 0 || s->Hq <= 0 || s->Hkv <= 0 || s->Hq % s->Hkv || s->T <= 0 || s->N < s->T) return PYR_EINVAL;
   if (s->dtype != PYR_F32 && s->dtype != PYR_BF16) return PYR_EUNSUPPORTED;
   if (s->d != 64 && s->d != 128) return PYR_EUNSUPPORTED;
-  if (s->T > kTreeMaxT || s->B > 4096 || s->Hq > 65535 || s->N > (1 << 28)) return PYR_EUNSUPPORTED;
+  if (s->T > kTreeMaxT || s->B > kTreeMaxB || s->Hq > 65535 || s->N > (1 << 28)) return PYR_EUNSUPPORTED;
   TreeGeo t = {s->B, s->Hq, s->Hkv, s->Hq / s->Hkv, s->N, s->T, s->d, s->dtype};
   if (t.dtype == PYR_BF16) {
     // one CTA per SM (148): two 128-row tiles where the group's heads do not fit in one

@@ -26,7 +26,7 @@ struct TreeArgs {
   int* status;
 };
 
-constexpr int kTreeMaxT = 64;
+constexpr int kTreeMaxT = 64, kTreeMaxB = 4096;
 
 // head of the group and token of row rr of row group rg; false: the row holds nothing
 __device__ __forceinline__ bool tree_row(const TreeGeo& g, int rg, int rr, int* h, int* t) {

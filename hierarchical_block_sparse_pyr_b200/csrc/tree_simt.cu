@@ -106,10 +106,11 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
 template <int D, int ROWS>
 cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
   auto kern = tree_simt_kernel<float, D, ROWS>;
-  const int smem = tree_smem<D, ROWS>() + (g.B + 1) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the kernel's, not the call's: the same in every call, as two threads may be here at once
+  constexpr int most = tree_smem<D, ROWS>() + (kTreeMaxB + 1) * 4;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
-  kern<<<g.C, 4 * ROWS, smem, st>>>(g, a);
+  kern<<<g.C, 4 * ROWS, tree_smem<D, ROWS>() + (g.B + 1) * 4, st>>>(g, a);
   return cudaGetLastError();
 }
 

@@ -497,10 +497,12 @@ cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
       !make_tmap_bf16_view(&mv, a.v.data, a.v.batch, a.v.head, a.v.row, D, g.N, g.Hkv, g.B, 128))
     return cudaErrorInvalidValue;
   auto kern = tree_tc_kernel<D, SPLIT>;
-  const int smem = TPlan<D, SPLIT>::kBytes + 4 * (g.B + 1);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the kernel's, not the call's: the same in every call, as two threads may be here at once
+  constexpr int most = TPlan<D, SPLIT>::kBytes + 4 * (kTreeMaxB + 1);
+  static_assert(most <= 227 * 1024, "shared memory of a CTA");
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
-  kern<<<g.C, kThreads, smem, st>>>(mq, mk, mv, g, a, heads * g.T * D * 2);
+  kern<<<g.C, kThreads, TPlan<D, SPLIT>::kBytes + 4 * (g.B + 1), st>>>(mq, mk, mv, g, a, heads * g.T * D * 2);
   return cudaGetLastError();
 }
 
