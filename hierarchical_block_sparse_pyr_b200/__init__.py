@@ -429,8 +429,9 @@ def _device_of(t):
     return t.get_device() if isinstance(t, torch.Tensor) else -1
 
 
-def _plain(t, name, dtype, numel, device):
-    """Pointer of a contiguous tensor of one dtype with at least numel elements (None: NULL)."""
+def _plain(t, name, dtype, need, device):
+    """Pointer of a contiguous tensor of one dtype (None: NULL) of the shape `need` (a tuple), or of at least `need`
+    elements in any shape (an int: buffers)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -439,15 +440,18 @@ def _plain(t, name, dtype, numel, device):
         raise TypeError(f"{name} must have dtype {dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on another device than the other operands")
-    if not t.is_contiguous() or t.numel() < numel:
-        raise ValueError(f"{name} must be contiguous with at least {numel} elements")
+    if need.__class__ is tuple:
+        if t.shape != need or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with shape {need}, not {tuple(t.shape)}")
+    elif not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"{name} must be contiguous with at least {need} elements")
     return t.data_ptr()
 
 
-def _need(t, name, dtype, numel, device):
+def _need(t, name, dtype, need, device):
     if t is None:
         raise ValueError(f"{name} is required")
-    return _plain(t, name, dtype, numel, device)
+    return _plain(t, name, dtype, need, device)
 
 
 def _call(fn, what, device, stream, *args):
@@ -480,8 +484,9 @@ def rope_spec(d: int, rot: int = None, base: float = 10000.0, layout: str = "hal
     if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
         raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
     spec = RopeSpec()
-    _check(_L().rope_spec_init(ctypes.byref(spec), int(d), int(d if rot is None else rot), _ROPE_LAYOUTS[layout],
-                               float(base), _ROPE_SCALINGS[scaling], float(factor), int(trained)), "rope_spec")
+    _check(_L().rope_spec_init(ctypes.byref(spec), int(d), int(d if rot is None else rot),
+                               _ROPE_LAYOUTS[layout], float(base), _ROPE_SCALINGS[scaling], float(factor),
+                               int(trained)), "rope_spec")
     return spec
 
 
@@ -505,7 +510,7 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
             continue
         if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[1] < 1:
             raise ValueError(f"{name} must be [B, H, N, d]")
-        heads[i] = x.shape[1]
+        heads[i] = int(x.shape[1])
         shape = (B, heads[i], N, d)
         operands += ((x, name, shape), (y, name + "o", shape))
     arr, v = _views(dt, dev, *operands)
@@ -524,7 +529,8 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
 
 def packed_shape(S: int, T: int, Hq: int, Hkv: int, d: int, dtype) -> PackedShape:
     """S sequences on a token axis of T tokens (the last sequence may end before T)."""
-    return PackedShape(int(S), int(T), int(Hq), int(Hkv), int(d), _dtype_code(dtype))
+    return PackedShape(int(S), int(T), int(Hq), int(Hkv), int(d),
+                       _dtype_code(dtype))
 
 
 def packed_plan_elems(s: PackedShape) -> int:
@@ -545,7 +551,7 @@ def packed_plan(s: PackedShape, cu, plan=None, status=None, stream=None):
     and packed_backward of this shape and these boundaries. Returns plan (allocated if None, as memory of the
     stream that writes it: another stream's user waits for that stream and keeps the plan until it is done)."""
     dev = _device_of(cu)
-    c = _need(cu, "cu", torch.int32, s.S + 1, dev)
+    c = _need(cu, "cu", torch.int32, (s.S + 1,), dev)
     n = packed_plan_elems(s)
     if plan is None:
         with torch.cuda.stream(_torch_stream(stream, dev)):
@@ -563,7 +569,7 @@ def packed_forward(s: PackedShape, Q, K, V, plan, O, lse=None, status=None, stre
     arr, v = _views(s.dtype, dev, (Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q))
     _call(_L().packed_forward, "packed_forward", dev, stream, ctypes.byref(s), v, v + 32, v + 64,
           _need(plan, "plan", torch.int32, _plan_words(s), dev), v + 96,
-          _plain(lse, "lse", torch.float32, s.Hq * s.T, dev), _plain(status, "status", torch.int32, 1, dev))
+          _plain(lse, "lse", torch.float32, (s.Hq, s.T), dev), _plain(status, "status", torch.int32, 1, dev))
 
 
 def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV, status=None, stream=None):
@@ -573,7 +579,7 @@ def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV
     q, kv = (s.Hq, s.T, s.d), (s.Hkv, s.T, s.d)
     arr, v = _views(s.dtype, dev, (Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q), (dO, "dO", q), (dQ, "dQ", q),
                     (dK, "dK", kv), (dV, "dV", kv))
-    n = s.Hq * s.T
+    n = (s.Hq, s.T)
     _call(_L().packed_backward, "packed_backward", dev, stream, ctypes.byref(s), v, v + 32, v + 64,
           _need(plan, "plan", torch.int32, _plan_words(s), dev), v + 96, _need(lse, "lse", torch.float32, n, dev),
           v + 128, _need(delta, "delta", torch.float32, n, dev), v + 160, v + 192, v + 224,
@@ -582,7 +588,8 @@ def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV
 
 def tree_shape(B: int, Hq: int, Hkv: int, N: int, T: int, d: int, dtype) -> TreeShape:
     """T drafted tokens of each of B sequences over caches of N rows."""
-    return TreeShape(int(B), int(Hq), int(Hkv), int(N), int(T), int(d), _dtype_code(dtype))
+    return TreeShape(int(B), int(Hq), int(Hkv), int(N), int(T),
+                     int(d), _dtype_code(dtype))
 
 
 def tree_workspace_bytes(s: TreeShape) -> int:
@@ -598,8 +605,8 @@ def tree_forward(s: TreeShape, Q, K, V, lens, parent, O, lse=None, workspace=Non
     arr, v = _views(s.dtype, dev, (Q, "Q", q), (K, "K", kv), (V, "V", kv), (O, "O", q))
     w = _need(workspace, "workspace", torch.uint8, 0, dev)
     _call(_L().tree_forward, "tree_forward", dev, stream, ctypes.byref(s), v, v + 32, v + 64,
-          _need(lens, "lens", torch.int32, s.B, dev), _plain(parent, "parent", torch.int32, s.B * s.T, dev), v + 96,
-          _plain(lse, "lse", torch.float32, s.B * s.Hq * s.T, dev), w, workspace.numel(),
+          _need(lens, "lens", torch.int32, (s.B,), dev), _plain(parent, "parent", torch.int32, (s.B, s.T), dev), v + 96,
+          _plain(lse, "lse", torch.float32, (s.B, s.Hq, s.T), dev), w, workspace.numel(),
           _plain(status, "status", torch.int32, 1, dev))
 
 

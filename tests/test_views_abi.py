@@ -167,3 +167,70 @@ def test_python_refusals():
     t = P.tree_shape(1, 2, 2, 8, 1, 64, F32)
     with pytest.raises(TypeError):
         P.tree_forward(t, x[None, :, :1], x[None], x[None], None, None, x[None, :, :1])
+
+
+class _OnDevice(torch.Tensor):
+    """A CPU tensor that says it is on device 0: the host's checks without a GPU."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def _dev(shape, dtype=F32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(_OnDevice)
+
+
+@pytest.fixture
+def stop(monkeypatch):
+    """Calls end where the library would be entered."""
+    class Reached(Exception):
+        pass
+
+    def call(*a):
+        raise Reached
+
+    monkeypatch.setattr(P, "_call", call)
+    return Reached
+
+
+def test_shapes_of_plain_operands(stop):
+    """Tensors of the right number of elements in another shape, or padded, are refused: the kernels would read
+    or write them with the wrong pitch."""
+    I = torch.int32
+    s = P.packed_shape(3, 8, 4, 2, 64, F32)
+    q, k = _dev((4, 8, 64)), _dev((2, 8, 64))
+    cu, plan, lse = _dev((4,), I), _dev((P.packed_plan_elems(s),), I), _dev((4, 8))
+    with pytest.raises(stop):
+        P.packed_plan(s, cu, plan)
+    with pytest.raises(stop):
+        P.packed_forward(s, q, k, k, plan, q, lse)
+    with pytest.raises(stop):
+        P.packed_forward(s, q, k, k, _dev((plan.numel() + 100,), I), q)  # a longer buffer holds a plan as well
+    with pytest.raises(stop):
+        P.packed_backward(s, q, k, k, plan, q, lse, q, lse, q, k, k)
+    for bad in (_dev((3,), I), _dev((5,), I), _dev((2, 2), I), _dev((4, 1), I)):
+        with pytest.raises(ValueError):
+            P.packed_plan(s, bad, plan)
+    for bad in (_dev((8, 4)), _dev((4, 10)), _dev((32,)), _dev((1, 4, 8)), _dev((4, 7))):
+        with pytest.raises(ValueError):
+            P.packed_forward(s, q, k, k, plan, q, bad)
+        with pytest.raises(ValueError):
+            P.packed_backward(s, q, k, k, plan, q, bad, q, lse, q, k, k)
+        with pytest.raises(ValueError):
+            P.packed_backward(s, q, k, k, plan, q, lse, q, bad, q, k, k)
+    t = P.tree_shape(3, 4, 2, 20, 5, 64, F32)
+    q, k = _dev((3, 4, 5, 64)), _dev((3, 2, 20, 64))
+    lens, parent, lse = _dev((3,), I), _dev((3, 5), I), _dev((3, 4, 5))
+    ws = _dev((P.tree_workspace_bytes(t) + 64,), torch.uint8)
+    with pytest.raises(stop):
+        P.tree_forward(t, q, k, k, lens, parent, q, lse, ws)
+    for bad in (_dev((5, 3), I), _dev((15,), I), _dev((3, 6), I), _dev((4, 5), I)):
+        with pytest.raises(ValueError):
+            P.tree_forward(t, q, k, k, lens, bad, q, lse, ws)
+    for bad in (_dev((4,), I), _dev((3, 1), I)):
+        with pytest.raises(ValueError):
+            P.tree_forward(t, q, k, k, bad, parent, q, lse, ws)
+    for bad in (_dev((3, 5, 4)), _dev((3, 4, 6)), _dev((60,))):
+        with pytest.raises(ValueError):
+            P.tree_forward(t, q, k, k, lens, parent, q, bad, ws)
