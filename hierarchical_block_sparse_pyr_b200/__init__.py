@@ -389,7 +389,7 @@ def _dtype_code(dtype):
         if dtype not in _DTYPES:
             raise TypeError(f"dtype must be float32 or bfloat16, not {dtype}")
         return _DTYPES[dtype]
-    return int(dtype)
+    return _int32(dtype, "dtype")
 
 
 _TORCH_DTYPES = {v: k for k, v in _DTYPES.items()}
@@ -454,6 +454,14 @@ def _need(t, name, dtype, need, device):
     return _plain(t, name, dtype, need, device)
 
 
+def _int32(x, name):
+    """x as the library's 32-bit integer; ctypes would wrap one that does not fit."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit in 32 bits")
+    return x
+
+
 def _call(fn, what, device, stream, *args):
     """fn(*args, stream) with the operands' device current; stream None: that device's current stream."""
     if torch.cuda.current_device() != device:
@@ -484,9 +492,9 @@ def rope_spec(d: int, rot: int = None, base: float = 10000.0, layout: str = "hal
     if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
         raise ValueError(f"unknown layout {layout!r} or scaling {scaling!r}")
     spec = RopeSpec()
-    _check(_L().rope_spec_init(ctypes.byref(spec), int(d), int(d if rot is None else rot),
+    _check(_L().rope_spec_init(ctypes.byref(spec), _int32(d, "d"), _int32(d if rot is None else rot, "rot"),
                                _ROPE_LAYOUTS[layout], float(base), _ROPE_SCALINGS[scaling], float(factor),
-                               int(trained)), "rope_spec")
+                               _int32(trained, "trained")), "rope_spec")
     return spec
 
 
@@ -503,6 +511,8 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
     B, _, N, d = first.shape
     if d != spec.d:
         raise ValueError(f"the spec is for d = {spec.d}, not {d}")
+    _int32(B, "B")
+    _int32(N, "N")
     dt, dev = _dtype_code(first.dtype), first.get_device()
     operands, heads = [], [0, 0]
     for i, (x, y, name) in enumerate(((Q, Qo, "Q"), (K, Ko, "K"))):
@@ -510,7 +520,7 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
             continue
         if not isinstance(x, torch.Tensor) or x.dim() != 4 or x.shape[1] < 1:
             raise ValueError(f"{name} must be [B, H, N, d]")
-        heads[i] = int(x.shape[1])
+        heads[i] = _int32(x.shape[1], "heads")
         shape = (B, heads[i], N, d)
         operands += ((x, name, shape), (y, name + "o", shape))
     arr, v = _views(dt, dev, *operands)
@@ -524,12 +534,12 @@ def rope_apply(spec: RopeSpec, Q, K, Qo, Ko, pos=None, pos_offset: int = 0, inve
             raise ValueError("pos must be [B, N] or [N]")
         stride = N if pos.dim() == 2 else 0
     _call(_L().rope_apply, "rope_apply", dev, stream, ctypes.byref(spec), B, heads[0], heads[1], N, dt, q, k, p, stride,
-          int(pos_offset), qo, ko, int(bool(inverse)), _plain(status, "status", torch.int32, 1, dev))
+          _int32(pos_offset, "pos_offset"), qo, ko, int(bool(inverse)), _plain(status, "status", torch.int32, 1, dev))
 
 
 def packed_shape(S: int, T: int, Hq: int, Hkv: int, d: int, dtype) -> PackedShape:
     """S sequences on a token axis of T tokens (the last sequence may end before T)."""
-    return PackedShape(int(S), int(T), int(Hq), int(Hkv), int(d),
+    return PackedShape(_int32(S, "S"), _int32(T, "T"), _int32(Hq, "Hq"), _int32(Hkv, "Hkv"), _int32(d, "d"),
                        _dtype_code(dtype))
 
 
@@ -588,8 +598,8 @@ def packed_backward(s: PackedShape, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV
 
 def tree_shape(B: int, Hq: int, Hkv: int, N: int, T: int, d: int, dtype) -> TreeShape:
     """T drafted tokens of each of B sequences over caches of N rows."""
-    return TreeShape(int(B), int(Hq), int(Hkv), int(N), int(T),
-                     int(d), _dtype_code(dtype))
+    return TreeShape(_int32(B, "B"), _int32(Hq, "Hq"), _int32(Hkv, "Hkv"), _int32(N, "N"), _int32(T, "T"),
+                     _int32(d, "d"), _dtype_code(dtype))
 
 
 def tree_workspace_bytes(s: TreeShape) -> int:

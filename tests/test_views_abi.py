@@ -234,3 +234,30 @@ def test_shapes_of_plain_operands(stop):
     for bad in (_dev((3, 5, 4)), _dev((3, 4, 6)), _dev((60,))):
         with pytest.raises(ValueError):
             P.tree_forward(t, q, k, k, lens, parent, q, bad, ws)
+
+
+def test_integers_that_do_not_fit(stop):
+    """The library takes 32-bit integers: one that does not fit is refused, not wrapped into another value."""
+    x = _dev((1, 2, 8, 64))
+    spec = P.rope_spec(64)
+    with pytest.raises(stop):
+        P.rope_apply(spec, x, None, x, None, pos_offset=-5)
+    for off in (2 ** 32 + 5, -2 ** 31 - 1, 2 ** 31):
+        with pytest.raises(ValueError):
+            P.rope_apply(spec, x, None, x, None, pos_offset=off)
+    for i in range(5):
+        a = [1, 8, 2, 2, 64]
+        a[i] += 2 ** 32
+        with pytest.raises(ValueError):
+            P.packed_shape(*a, F32)
+    for i in range(6):
+        a = [1, 2, 2, 8, 1, 64]
+        a[i] += 2 ** 32
+        with pytest.raises(ValueError):
+            P.tree_shape(*a, F32)
+    for kw in (dict(d=2 ** 32 + 64), dict(d=64, rot=2 ** 32 + 32),
+               dict(d=64, scaling="yarn", factor=2.0, trained=2 ** 32 + 8192)):
+        with pytest.raises(ValueError):
+            P.rope_spec(**kw)
+    with pytest.raises(ValueError):
+        P.packed_shape(1, 8, 2, 2, 64, 2 ** 32)
