@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(256) packed_delta_kernel(PackedGeo g, PackedBw
   const int4 w = reinterpret_cast<const int4*>(a.plan + packed_list_at(g, kListQ))[tile];
   const int lane = threadIdx.x % L;
   const int stop = min(w.z + packed_tile_rows(g, kListQ), w.y);
-  for (int t0 = w.z + threadIdx.x / L; t0 < stop; t0 += U * (256 / L)) {
+  // the loop is the block's as a whole: the sums below are exchanged by whole warps, whose rows may end at different t
+  for (int base = w.z; base < stop; base += U * (256 / L)) {
+    const int t0 = base + threadIdx.x / L;
     uint4 o[U], d[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {

@@ -152,3 +152,29 @@ def test_a_query_that_is_not_a_number(dtype, d, Hq, Hkv):
     clean = torch.cat([torch.arange(cu[i], cu[i + 1]) for i in range(1, 2 * L, 2)]).cuda()
     for x, y in zip((dQ, dK, dV), want[2]):
         assert torch.equal(x[:, clean], y[:, clean])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_delta_of_every_length(dtype, d):
+    """delta for sequences of 1 to 140 tokens: a row's sum is exchanged by lanes of a warp whose other rows may be
+    behind the sequence's end. dO . O is a sum of d products in fp32 of values exact in it: at most d 2^-24 of the sum
+    of their magnitudes off; bf16 then takes sum_k P (dO . v), which is dO . O of the O in double, with P, dO . v and
+    their sum in fp32 (the exponents are off by 2^-24 (8 + d / 8) |q||k| / sqrt(d) at most, the exponentials on the FMA
+    pipe by 1.0e-4 of themselves, and |dO . v - D| is at most twice |dO| max |v|)."""
+    lens = list(range(1, 141))
+    cu, Q, K, V, dO = _make(lens, 2, 1, d, dtype, 13)
+    Q, K, V, dO = (x.to(dtype) for x in (Q, K, V, dO))
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    T = cu[-1]
+    s = P.packed_shape(len(lens), T, 2, 1, d, dtype)
+    plan = P.packed_plan(s, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    O, lse, delta = torch.empty_like(Q), torch.empty((2, T), device="cuda"), torch.full((2, T), 7.0, device="cuda")
+    P.packed_forward(s, Q, K, V, plan, O, lse)
+    P.packed_backward(s, Q, K, V, plan, O, lse, dO, delta, *(torch.empty_like(x) for x in (Q, K, V)))
+    o, _ = ref.packed(Q, K, V, cu)
+    want, size = (dO.double() * o).sum(-1), dO.double().norm(dim=-1) * V.double().norm(dim=-1).max()
+    score = Q.double().norm(dim=-1).max() * K.double().norm(dim=-1).max() / math.sqrt(d)
+    bound = (2.0 ** -24 * (d + (8 + d / 8) * score) + (2.0e-4 if dtype == BF16 else 0)) * size
+    assert ((delta.double() - want).abs() <= bound).all()
