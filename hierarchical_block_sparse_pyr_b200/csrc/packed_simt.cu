@@ -49,7 +49,7 @@ constexpr int fwd_smem() {
 }
 
 // S = Q K^T, online softmax, O += P V over 64-key tiles; P goes over K's buffer.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads<D>) packed_fwd_simt_kernel(PackedGeo g, PackedFwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm, *Ks = Qs + kRows * (D + 4) + team() * fwd_team<D>(), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads<D>) packed_fwd_simt_kernel(PackedGeo 
   const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float sl2 = rsqrtf((float)D) * kLog2e;
   const int nrow = min(kRows, end - row0);
-  load_rows<kThreads<D>, T, D, kRows>(Qs, D + 4, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<kThreads<D>, D, kRows>(Qs, D + 4, view_at<float>(a.q, 0, h, row0), a.q.row, nrow);
   __syncthreads();
   float m[4], l[4], acc[4][D / 16];
 #pragma unroll
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kThreads<D>) packed_fwd_simt_kernel(PackedGeo 
   for (int k0 = start + team() * kTile; k0 < stop; k0 += kTeams<D> * kTile) {
     const int nk = min(kTile, stop - k0);
     team_sync();
-    load_rows<kTeam, T, D, kTile>(Ks, D + 4, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
-    load_rows<kTeam, T, D, kTile>(Vs, D, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    load_rows<kTeam, D, kTile>(Ks, D + 4, view_at<float>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<kTeam, D, kTile>(Vs, D, view_at<float>(a.v, 0, hk, k0), a.v.row, nk);
     team_sync();
     float s[4][4];
     mul_nt<kTeam, D>(s, Qs, D + 4, Ks, D + 4);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads<D>) packed_fwd_simt_kernel(PackedGeo 
 #pragma unroll
       for (int c = 0; c < D / 16; c++) acc[i][c] = acc[i][c] * f0 + got_acc<D>(buf, i, c) * f1;
     }
-    store_row<T, D>(view_at<T>(a.o, 0, h, t), acc[i], 1.f / l[i]);
+    store_row<D>(view_at<float>(a.o, 0, h, t), acc[i], 1.f / l[i]);
     if (a.lse && tx == 0) a.lse[(int64_t)h * g.T + t] = (m[i] + log2f(l[i])) * 0.6931471805599453f;
   }
 }
@@ -168,7 +168,7 @@ constexpr int bwd_smem() {
 }
 
 // dS = P (dO V^T - delta), dQ += dS K
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads<D>) packed_dq_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kThreads<D>) packed_dq_simt_kernel(PackedGeo g
   const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
   const int nrow = min(kRows, end - row0);
-  load_rows<kThreads<D>, T, D, kRows>(Qs, P, view_at<T>(a.q, 0, h, row0), a.q.row, nrow);
-  load_rows<kThreads<D>, T, D, kRows>(Gs, P, view_at<T>(a.dout, 0, h, row0), a.dout.row, nrow);
+  load_rows<kThreads<D>, D, kRows>(Qs, P, view_at<float>(a.q, 0, h, row0), a.q.row, nrow);
+  load_rows<kThreads<D>, D, kRows>(Gs, P, view_at<float>(a.dout, 0, h, row0), a.dout.row, nrow);
   float lse2[4], del[4], acc[4][D / 16];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(kThreads<D>) packed_dq_simt_kernel(PackedGeo g
   for (int k0 = start + team() * kTile; k0 < stop; k0 += kTeams<D> * kTile) {
     const int nk = min(kTile, stop - k0);
     team_sync();
-    load_rows<kTeam, T, D, kTile>(Ks, P, view_at<T>(a.k, 0, hk, k0), a.k.row, nk);
-    load_rows<kTeam, T, D, kTile>(Vs, P, view_at<T>(a.v, 0, hk, k0), a.v.row, nk);
+    load_rows<kTeam, D, kTile>(Ks, P, view_at<float>(a.k, 0, hk, k0), a.k.row, nk);
+    load_rows<kTeam, D, kTile>(Vs, P, view_at<float>(a.v, 0, hk, k0), a.v.row, nk);
     team_sync();
     float s[4][4], dp[4][4];
     mul_nt<kTeam, D>(s, Qs, P, Ks, P);
@@ -242,12 +242,12 @@ __global__ void __launch_bounds__(kThreads<D>) packed_dq_simt_kernel(PackedGeo g
     for (int k = 0; k < kTeams<D> - 1; k++)
 #pragma unroll
       for (int c = 0; c < D / 16; c++) acc[i][c] += got_acc<D>(sm + k * kRows * D, i, c);
-    if (row0 + 4 * ty + i < end) store_row<T, D>(view_at<T>(a.dq, 0, h, row0 + 4 * ty + i), acc[i], scale);
+    if (row0 + 4 * ty + i < end) store_row<D>(view_at<float>(a.dq, 0, h, row0 + 4 * ty + i), acc[i], scale);
   }
 }
 
 // rows = keys, columns = queries: dV += P^T dO, dK += dS^T Q over the rows of the group's heads
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads<D>) packed_dkdv_simt_kernel(PackedGeo g, PackedBwdArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int P = D + 4;
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kThreads<D>) packed_dkdv_simt_kernel(PackedGeo
   const int tx = threadIdx.x & 15, ty = team_tid<kTeam>() >> 4;
   const float scale = rsqrtf((float)D), sl2 = scale * kLog2e;
   const int nk = min(kRows, end - key0);
-  load_rows<kThreads<D>, T, D, kRows>(Ks, P, view_at<T>(a.k, 0, hk, key0), a.k.row, nk);
-  load_rows<kThreads<D>, T, D, kRows>(Vs, P, view_at<T>(a.v, 0, hk, key0), a.v.row, nk);
+  load_rows<kThreads<D>, D, kRows>(Ks, P, view_at<float>(a.k, 0, hk, key0), a.k.row, nk);
+  load_rows<kThreads<D>, D, kRows>(Vs, P, view_at<float>(a.v, 0, hk, key0), a.v.row, nk);
   __syncthreads();
   float dk[4][D / 16], dv[4][D / 16];
 #pragma unroll
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(kThreads<D>) packed_dkdv_simt_kernel(PackedGeo
     const int h = hk * g.G + step / nq_tiles, q0 = key0 + step % nq_tiles * kTile;
     const int nq = min(kTile, end - q0);
     team_sync();
-    load_rows<kTeam, T, D, kTile>(Qs, P, view_at<T>(a.q, 0, h, q0), a.q.row, nq);
-    load_rows<kTeam, T, D, kTile>(Gs, P, view_at<T>(a.dout, 0, h, q0), a.dout.row, nq);
+    load_rows<kTeam, D, kTile>(Qs, P, view_at<float>(a.q, 0, h, q0), a.q.row, nq);
+    load_rows<kTeam, D, kTile>(Gs, P, view_at<float>(a.dout, 0, h, q0), a.dout.row, nq);
     team_sync();
     float s[4][4], dp[4][4];
     mul_nt<kTeam, D>(s, Ks, P, Qs, P);
@@ -315,8 +315,8 @@ __global__ void __launch_bounds__(kThreads<D>) packed_dkdv_simt_kernel(PackedGeo
         dv[i][c] += got_acc<D>(sm + (2 * k + 1) * kRows * D, i, c);
       }
     if (4 * ty + i >= nk) continue;
-    store_row<T, D>(view_at<T>(a.dk, 0, hk, key0 + 4 * ty + i), dk[i], scale);
-    store_row<T, D>(view_at<T>(a.dv, 0, hk, key0 + 4 * ty + i), dv[i], 1.f);
+    store_row<D>(view_at<float>(a.dk, 0, hk, key0 + 4 * ty + i), dk[i], scale);
+    store_row<D>(view_at<float>(a.dv, 0, hk, key0 + 4 * ty + i), dv[i], 1.f);
   }
 }
 
@@ -330,20 +330,20 @@ cudaError_t launch(K kern, int64_t blocks, int threads, int smem, const PackedGe
   return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_bwd(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
   const cudaError_t e =
-      launch(packed_dq_simt_kernel<T, D>, packed_list_cap(g, kListQ) * g.Hq, kThreads<D>, bwd_smem<D>(), g, a, st);
+      launch(packed_dq_simt_kernel<D>, packed_list_cap(g, kListQ) * g.Hq, kThreads<D>, bwd_smem<D>(), g, a, st);
   if (e != cudaSuccess) return e;
-  return launch(packed_dkdv_simt_kernel<T, D>, packed_list_cap(g, kListK) * g.Hkv, kThreads<D>, bwd_smem<D>(), g, a, st);
+  return launch(packed_dkdv_simt_kernel<D>, packed_list_cap(g, kListK) * g.Hkv, kThreads<D>, bwd_smem<D>(), g, a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_packed_fwd_simt(const PackedGeo& g, const PackedFwdArgs& a, cudaStream_t st) {
   const int64_t blocks = packed_list_cap(g, kListFwd) * g.Hq;
-  return g.d == 64 ? launch(packed_fwd_simt_kernel<float, 64>, blocks, kThreads<64>, fwd_smem<64>(), g, a, st)
-                   : launch(packed_fwd_simt_kernel<float, 128>, blocks, kThreads<128>, fwd_smem<128>(), g, a, st);
+  return g.d == 64 ? launch(packed_fwd_simt_kernel<64>, blocks, kThreads<64>, fwd_smem<64>(), g, a, st)
+                   : launch(packed_fwd_simt_kernel<128>, blocks, kThreads<128>, fwd_smem<128>(), g, a, st);
 }
 
 cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
@@ -356,7 +356,7 @@ cudaError_t launch_packed_delta(const PackedGeo& g, const PackedBwdArgs& a, cuda
 }
 
 cudaError_t launch_packed_bwd_simt(const PackedGeo& g, const PackedBwdArgs& a, cudaStream_t st) {
-  return g.d == 64 ? launch_bwd<float, 64>(g, a, st) : launch_bwd<float, 128>(g, a, st);
+  return g.d == 64 ? launch_bwd<64>(g, a, st) : launch_bwd<128>(g, a, st);
 }
 
 }  // namespace pyr

@@ -17,31 +17,21 @@ template <int NT>
 __device__ __forceinline__ int team_tid() { return threadIdx.x & (NT - 1); }
 
 // dst[r][0 .. D) = row r of src where wanted(r), zeros in the other of the N rows
-template <int NT, typename T, int D, int N, typename F>
-__device__ __forceinline__ void load_rows_if(float* dst, int pitch, const T* src, int64_t stride, F wanted) {
-  constexpr int E = 16 / sizeof(T), C = D / E;
+template <int NT, int D, int N, typename F>
+__device__ __forceinline__ void load_rows_if(float* dst, int pitch, const float* src, int64_t stride, F wanted) {
+  constexpr int C = D / 4;
 #pragma unroll 4
   for (int x = team_tid<NT>(); x < N * C; x += NT) {
-    const int r = x / C, c = x - r * C;
-    float* d = dst + r * pitch + c * E;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (wanted(r)) v = *reinterpret_cast<const uint4*>(src + r * stride + c * E);
-    if (sizeof(T) == 4) {
-      *reinterpret_cast<uint4*>(d) = v;
-    } else {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        d[2 * i] = __uint_as_float(w[i] << 16);
-        d[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
+    const int r = x / C, c = 4 * (x - r * C);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (wanted(r)) v = *reinterpret_cast<const float4*>(src + r * stride + c);
+    *reinterpret_cast<float4*>(dst + r * pitch + c) = v;
   }
 }
 
-template <int NT, typename T, int D, int N>
-__device__ __forceinline__ void load_rows(float* dst, int pitch, const T* src, int64_t stride, int n) {
-  load_rows_if<NT, T, D, N>(dst, pitch, src, stride, [n](int r) { return r < n; });
+template <int NT, int D, int N>
+__device__ __forceinline__ void load_rows(float* dst, int pitch, const float* src, int64_t stride, int n) {
+  load_rows_if<NT, D, N>(dst, pitch, src, stride, [n](int r) { return r < n; });
 }
 
 // acc[i][j] = A[4 ty + i] . B[tx + 16 j] over D elements
@@ -139,22 +129,14 @@ __device__ __forceinline__ void softmax_step(float (&s)[4][4], float (&m)[4], fl
   }
 }
 
-// row 4 ty + i of a 64 x D accumulator, times f, to a row of T
-template <typename T, int D>
-__device__ __forceinline__ void store_row(T* dst, const float (&acc)[D / 16], float f) {
+// row 4 ty + i of a 64 x D accumulator, times f, to memory
+template <int D>
+__device__ __forceinline__ void store_row(float* dst, const float (&acc)[D / 16], float f) {
   const int tx = threadIdx.x & 15;
 #pragma unroll
-  for (int j = 0; j < D / 64; j++) {
-    const float x[4] = {acc[4 * j] * f, acc[4 * j + 1] * f, acc[4 * j + 2] * f, acc[4 * j + 3] * f};
-    if (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(dst) + 4 * tx + 64 * j) =
-          make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-      __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-      uint2 u = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(dst) + 4 * tx + 64 * j) = u;
-    }
-  }
+  for (int j = 0; j < D / 64; j++)
+    *reinterpret_cast<float4*>(dst + 4 * tx + 64 * j) =
+        make_float4(acc[4 * j] * f, acc[4 * j + 1] * f, acc[4 * j + 2] * f, acc[4 * j + 3] * f);
 }
 
 }  // namespace simt

@@ -152,7 +152,6 @@ __device__ __forceinline__ void tree_prefix(const TreeGeo& g, const TreeArgs& a,
 
 // masks[t] = the drafted tokens that token t sees (itself and its ancestors), 0 if the slot is absent, by
 // one warp. Pointer jumping: after k rounds a token has the 2^k nearest of its path.
-// buf: 2 * 64 uint64 and 64 ints of scratch in shared memory.
 struct TreeMaskBuf {
   unsigned long long mask[kTreeMaxT];
   int ptr[kTreeMaxT];  // next ancestor not yet merged; -1: none; -2: the path holds an absent slot

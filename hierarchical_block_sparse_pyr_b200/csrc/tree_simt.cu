@@ -15,7 +15,7 @@ constexpr int tree_smem() {
   return ((ROWS + kTile) * (D + 4) + kTile * D) * 4;
 }
 
-template <typename T, int D, int ROWS>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs a) {
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm, *Ks = Qs + ROWS * (D + 4), *Vs = Ks + kTile * (D + 4), *Ps = Ks;
@@ -35,11 +35,11 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
     __syncthreads();
     if (threadIdx.x < 32) tree_masks(g, a, b, good, &masks);
     const int nr = min(ROWS, g.G * g.T - r0);
-    for (int i = threadIdx.x; i < ROWS * (D / 8); i += 4 * ROWS) {
-      const int r = i / (D / 8), c = i - r * (D / 8), ra = r0 + r;
-      const T* src = r < nr ? view_at<T>(a.q, b, hk * g.G + ra / g.T, ra % g.T) + c * 8 : nullptr;
-#pragma unroll
-      for (int e = 0; e < 8; e++) Qs[r * (D + 4) + c * 8 + e] = src ? to_f32(src[e]) : 0.f;
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += 4 * ROWS) {
+      const int r = i / (D / 4), c = 4 * (i - r * (D / 4)), ra = r0 + r;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < nr) v = *reinterpret_cast<const float4*>(view_at<float>(a.q, b, hk * g.G + ra / g.T, ra % g.T) + c);
+      *reinterpret_cast<float4*>(Qs + r * (D + 4) + c) = v;
     }
     __syncthreads();
     const unsigned long long used = tree_used(&masks);
@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
         return good && (u < 0 || (u < g.T && ((used >> u) & 1)));
       };
       __syncthreads();
-      load_rows_if<4 * ROWS, T, D, kTile>(Ks, D + 4, view_at<T>(a.k, b, hk, k0), a.k.row, wanted);
-      load_rows_if<4 * ROWS, T, D, kTile>(Vs, D, view_at<T>(a.v, b, hk, k0), a.v.row, wanted);
+      load_rows_if<4 * ROWS, D, kTile>(Ks, D + 4, view_at<float>(a.k, b, hk, k0), a.k.row, wanted);
+      load_rows_if<4 * ROWS, D, kTile>(Vs, D, view_at<float>(a.v, b, hk, k0), a.v.row, wanted);
       __syncthreads();
       float s[4][4];
       mul_nt<4 * ROWS, D>(s, Qs, D + 4, Ks, D + 4);
@@ -91,12 +91,12 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
       }
       if (whole) {
         const int h = hk * g.G + (r0 + r) / g.T, t = (r0 + r) % g.T;
-        store_row<T, D>(view_at<T>(a.o, b, h, t), acc[i], l[i] != 0.f ? 1.f / l[i] : 0.f);
+        store_row<D>(view_at<float>(a.o, b, h, t), acc[i], l[i] != 0.f ? 1.f / l[i] : 0.f);
         if (a.lse && tx == 0)
           a.lse[((int64_t)b * g.Hq + h) * g.T + t] =
               l[i] != 0.f ? (m[i] + log2f(l[i])) * 0.6931471805599453f : -INFINITY;
       } else {
-        store_row<float, D>(a.part_o + (part + r) * D, acc[i], 1.f);
+        store_row<D>(a.part_o + (part + r) * D, acc[i], 1.f);
         if (tx == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * (part + r)) = make_float2(m[i], l[i]);
       }
     }
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(4 * ROWS) tree_simt_kernel(TreeGeo g, TreeArgs
 
 template <int D, int ROWS>
 cudaError_t launch(const TreeGeo& g, const TreeArgs& a, cudaStream_t st) {
-  auto kern = tree_simt_kernel<float, D, ROWS>;
+  auto kern = tree_simt_kernel<D, ROWS>;
   // the limit is the kernel's, not the call's: the same in every call, as two threads may be here at once
   constexpr int most = tree_smem<D, ROWS>() + (kTreeMaxB + 1) * 4;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
