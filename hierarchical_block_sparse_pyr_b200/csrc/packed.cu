@@ -37,7 +37,8 @@ __device__ int block_scan(int x, int* warp_sums, int* sum) {
 
 // One block writes the three lists. Each: tile counts summed over the sequences, then a counting sort of
 // all tiles by work in 2048 buckets. Tiles of one bucket come in no fixed order; every tile's result is
-// its own, so the order moves no bit of the output.
+// its own, so the order moves no bit of the output. Bound by the latency of its passes: 9 us for a few sequences (32K
+// tokens in 4), 14 us for 512 of 64 tokens, 44 us for 16 of 64K, 0.47 ms for 32768 of 8.
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedGeo g, const int32_t* __restrict__ cu,
                                                                    int32_t* __restrict__ plan, int* status) {
   __shared__ int hist[kBuckets];

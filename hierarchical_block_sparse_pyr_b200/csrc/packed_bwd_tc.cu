@@ -25,11 +25,11 @@
 //   rest = sum_k P (dP - delta)   makes   delta + rest = sum_k P dP   up to the rounding of the differences alone,
 // so it subtracts rest PK from dQ, and writes delta + rest back for the dK/dV kernel, which therefore runs second.
 // The rows of a sequence's first tile see one key tile: they get delta + rest before dS is formed, which leaves
-// exactly 0 where a row sees one key. (8192 tokens, 16 heads: without PK and rest 764 us for all of the gradients,
-// with them 830; sustained 32K tokens 7.7 and 8.5 ms.)
-// Measured (8192 tokens, 16 heads of 128): dK/dV 0.39 ms, 2850 cycles a step, tensor pipe 72 % busy, with shared
-// memory (256 KB a step, 2048 cycles) close behind; dQ 0.39 ms, where the softmax warps' chain of loads,
-// exponentials and stores is the bound, 2900 cycles a step against 2048 of products.
+// exactly 0 where a row sees one key. (8192 tokens, 16 heads, all of the gradients: without PK and rest 748 us, with
+// them 823.)
+// Measured (8192 tokens, 16 heads of 128): 2840 cycles a step in both kernels, tensor pipe 72 % busy, 0.4 ms each.
+// dK/dV has shared memory close behind (256 KB a step, 2048 cycles), dQ the softmax warps' chain of loads,
+// exponentials and stores. 32K tokens: 7.3 ms in a burst, 8.5 ms over a second, at the power cap.
 // Rows behind the sequence's end may hold anything. As rows of A they only reach outputs that are not
 // stored; where they are summed over (B of dK, dV and dQ) they are zeroed in shared memory.
 #include "packed.cuh"

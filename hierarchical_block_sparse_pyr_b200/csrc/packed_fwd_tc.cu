@@ -30,8 +30,9 @@ namespace {
 
 using namespace tc;
 
-// of 32 pairs of exponentials, on the FMA pipe. Kernel time against it is rugged (32K tokens, 16 heads, timed for
-// a second: none 2.53 ms, the last 10 2.33, 11 2.45, 12 2.26, 14 2.49, 12 spread evenly 2.31)
+// of 32 pairs of exponentials, on the FMA pipe. Kernel time against it is rugged at d = 128 (32K tokens, 16 heads,
+// timed for a second: none 2.53 ms, the last 10 2.33, 11 2.45, 12 2.26, 14 2.49, 12 spread evenly 2.31; 8K tokens, in a
+// burst: none 262 us, 8 248, 12 233, 14 262). At d = 64 (8K tokens): none 225 us, 8 203, 12 211, 14 217
 constexpr int kFma = 12;
 
 template <int D>

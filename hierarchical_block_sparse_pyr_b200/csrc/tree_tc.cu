@@ -10,9 +10,10 @@
 //   warps 0-3, 4-7  softmax of slot 0 and 1, one thread a row     warp 8   TMA
 //   warp 9          S = Q K^T     warp 10  O += P V               warp 11  the trees' masks
 // A row tile holds the T rows of 128 / T heads, in the order of the TMA box that loads them.
-// Measured (32/8 heads of 128): 32 sequences of 1 to 131056 tokens, 16 drafts: 1.02 ms, 6.8 TB/s in a burst, 1.23 ms
-// over a second of calls, at the power cap. 4 sequences of 511 to 32000, 64 drafts: 80 us, where the two slots'
-// softmax is the bound: they run in step, 3600 to 3850 cycles a step against 2048 of products.
+// Measured (32/8 heads of 128), whole calls with the join: 32 sequences of 1 to 131056 tokens, 16 drafts: 1.02 ms,
+// 6.8 TB/s in a burst, 1.23 ms over a second of calls, at the power cap; one token each: 0.98 and 1.18 ms. 4 sequences
+// of 511 to 32000, 64 drafts: 92 us in a burst, 96 over a second (this kernel alone 72 us under a profiler). No unit
+// is near its limit there: the two slots' softmax runs in step, 3600 to 3850 cycles against 2048 of products.
 // Rows of V that no token sees (behind the drafts, absent slots) are zeroed in shared memory before P V: the
 // cache may hold anything there, and 0 * NaN is NaN. Such rows of K only reach scores that are masked.
 #include "tc_softmax.cuh"

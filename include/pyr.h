@@ -550,7 +550,8 @@ PYR_API int packed_plan(const packed_shape* s, const int32_t* cu, int32_t* plan,
 
 /*
  * packed_forward - causal attention of every sequence of the batch.
- *   Q, O   views [Hq][T][d]; K, V views [Hkv][T][d] (batch strides ignored).
+ *   Q, O   views [Hq][T][d]; K, V views [Hkv][T][d] (batch strides ignored);
+ *          O overlaps no other operand.
  *   plan   device, as written by packed_plan for the same shape. A buffer that
  *          is not a plan of this shape gives no work, and PYR_EBADSEQ is
  *          reported in *dev_status.
@@ -606,7 +607,8 @@ PYR_API size_t tree_workspace_bytes(const tree_shape* s);
 
 /*
  * tree_forward - attention of the drafted tokens, softmax scale 1/sqrt(d).
- *   Q, O   views [B][Hq][T][d]; K, V views [B][Hkv][N][d].
+ *   Q, O   views [B][Hq][T][d]; K, V views [B][Hkv][N][d]; O overlaps no other
+ *          operand.
  *   len    device int32 [B]: cached context tokens, 0 <= len[b] and
  *          len[b] + T <= N. Drafted token t of sequence b has its key and value
  *          in row len[b] + t. A length out of range makes every slot of its
@@ -621,10 +623,12 @@ PYR_API size_t tree_workspace_bytes(const tree_shape* s);
  *          that share one must be ordered on a stream.
  * Cache rows at or behind len[b] + T are not used. A NaN in a query or a key
  * makes O and lse of the tokens that see it NaN; one in a value, or an infinity,
- * may reach all tokens of its sequence. The cache is read once per
- * key/value head for up to 256 query rows (T tokens of Hq / Hkv heads); the
- * work is split evenly over the GPU along the cached tokens and the parts are
- * joined in a fixed order.
+ * may reach all tokens of its sequence.
+ * The query rows of a key/value head (T tokens of G = Hq / Hkv heads) are
+ * worked on in parts, and the cache is read once for each: in bf16 a part has
+ * up to 2 floor(128 / T) whole heads, in fp32 up to 64 rows. The work is split
+ * evenly over the GPU along the cached tokens and the results of a part's
+ * pieces are joined in a fixed order.
  */
 PYR_API int tree_forward(const tree_shape* s, const pyr_view* Q, const pyr_view* K, const pyr_view* V,
                          const int32_t* len, const int32_t* parent, const pyr_view* O, float* lse, void* workspace,
