@@ -76,3 +76,64 @@ def test_plan_forward_and_backward_on_a_side_stream():
     for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
         for x, y in zip(run(stream), want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+def test_heads_whose_offsets_pass_32_bits(dtype):
+    """All operands as slices of one tensor whose heads are 2^31 elements apart (bytes and elements pass 32 bits)."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 9 GB of device memory")
+    g = torch.Generator().manual_seed(19)
+    cu, H, d = [0, 200, 201, 350], 2, 64
+    T = cu[-1]
+    flat = torch.empty(2 ** 31 + 8 * T * d, dtype=dtype, device="cuda")
+    far = [flat.as_strided((H, T, d), (2 ** 31, d, 1), i * T * d) for i in range(8)]
+    near = [torch.empty((H, T, d), dtype=dtype, device="cuda") for _ in range(8)]
+    s = P.packed_shape(3, T, H, H, d, dtype)
+    plan = P.packed_plan(s, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    for x, y in zip(far[:4], near[:4]):  # Q, K, V, dO
+        y.copy_(torch.randn((H, T, d), generator=g).to(dtype))
+        x.copy_(y)
+    for Q, K, V, dO, O, dQ, dK, dV in (far, near):
+        lse = torch.empty((H, T), device="cuda")
+        P.packed_forward(s, Q, K, V, plan, O, lse)
+        P.packed_backward(s, Q, K, V, plan, O, lse, dO, torch.empty_like(lse), dQ, dK, dV)
+    torch.cuda.synchronize()
+    for x, y in zip(far, near):
+        assert torch.equal(x, y)
+
+
+def test_one_plan_on_two_streams_at_once():
+    """The layers of a model share a plan; here two of them run at the same time."""
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    g = torch.Generator().manual_seed(29)
+    cu, Hq, Hkv, d = [0, 900, 1000, 2500], 8, 2, 64
+    T = cu[-1]
+    s = P.packed_shape(3, T, Hq, Hkv, d, BF16)
+    plan = P.packed_plan(s, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    layers = []
+    for _ in range(2):
+        Q, K, V, dO = (torch.randn((H, T, d), generator=g).to(BF16).cuda() for H in (Hq, Hkv, Hkv, Hq))
+        runs = [[torch.zeros_like(x) for x in (Q, Q, K, V)] + [torch.zeros((Hq, T), device="cuda") for _ in range(2)]
+                for _ in range(2)]
+        layers.append((Q, K, V, dO, runs, torch.cuda.Stream()))
+
+    def run(layer, out, stream):
+        Q, K, V, dO = layer[:4]
+        O, dQ, dK, dV, lse, delta = out
+        P.packed_forward(s, Q, K, V, plan, O, lse, stream=stream)
+        P.packed_backward(s, Q, K, V, plan, O, lse, dO, delta, dQ, dK, dV, stream=stream)
+
+    for layer in layers:
+        run(layer, layer[4][0], None)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for layer in layers:
+            run(layer, layer[4][1], layer[5])
+    torch.cuda.synchronize()
+    for layer in layers:
+        for x, y in zip(*layer[4]):
+            assert torch.equal(x, y)

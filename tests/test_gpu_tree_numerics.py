@@ -51,3 +51,24 @@ def test_a_key_that_is_not_a_number(dtype, lens, T, Hq, Hkv):
                 else:
                     assert torch.equal(O[b, :, t], want[0][b, :, t]), (row, b, t)
                     assert torch.equal(lse[b, :, t], want[1][b, :, t]), (row, b, t)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens,T", [([5000, 3, 900], 7), ([64, 70], 1), ([700] * 60, 33)])
+def test_what_the_workspace_held_does_not_matter(dtype, lens, T):
+    import hierarchical_block_sparse_pyr_b200 as P
+
+    B, Hq, Hkv, d = len(lens), 8, 2, 128
+    N = max(lens) + T
+    g = torch.Generator().manual_seed(14)
+    Q, K, V = (torch.randn((B, H, n, d), generator=g).to(dtype).cuda() for H, n in ((Hq, T), (Hkv, N), (Hkv, N)))
+    s = P.tree_shape(B, Hq, Hkv, N, T, d, dtype)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = []
+    for fill in (0, 255):  # 255: NaN in every part
+        ws = torch.full((P.tree_workspace_bytes(s),), fill, dtype=torch.uint8, device="cuda")
+        O, lse = torch.empty_like(Q), torch.empty((B, Hq, T), device="cuda")
+        P.tree_forward(s, Q, K, V, n, None, O, lse, ws)
+        out.append((O, lse))
+    torch.cuda.synchronize()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1]) and out[0][0].isfinite().all()
